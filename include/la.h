@@ -284,6 +284,101 @@ LA_API la_status la_prefill_backward_ex(const void* q, const void* k, const void
                                         size_t ws_bytes, la_stream_t stream);
 
 /*
+ * Linear attention with a decay for each head:
+ *
+ *     S_t = exp(g_h) S_{t-1} + k_t (x) v_t,   o_t = q_t S_t
+ *
+ * with log_decay = g: fp32 device [H] (4-byte aligned), one value per head h,
+ * g_h <= 0; g_h = 0 gives the calls without a decay, g_h = -infinity forgets
+ * everything (S_t = k_t (x) v_t).  The values are a precondition; a positive or
+ * NaN one is found only under LA_VALIDATE=1 (device-to-host copy and a stream
+ * sync).  g is a constant of the layer: there is no gradient for it.  The
+ * feature map is the identity.
+ *
+ * la_prefill_decay, la_prefill_varlen_decay and la_decode_step_decay are
+ * la_prefill, la_prefill_varlen and la_decode_step_ex with that recurrence: the
+ * same layouts, sizes, state formats, workspaces, aliasing rules and errors
+ * (a null log_decay is LA_ERR_INVALID_ARG).  Between two tokens n apart the
+ * weight is exp(n g) in chunks, segments and steps alike; it is formed in
+ * double and applied in fp32 to the scores, the outputs and the state.
+ * la_prefill_decay_backward is la_prefill_backward_ex for it: with
+ *   G_N = q_N^T dout_N + ds_n,  G_t = q_t^T dout_t + exp(g) G_{t+1},
+ *   dq_t = dout_t S_t^T,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  ds0 = exp(g) G_1
+ * (N = 0: ds0 = ds_n).
+ */
+LA_API size_t la_prefill_decay_workspace_size(int B, int H, int N, int dk, int dv, la_dtype dt);
+LA_API la_status la_prefill_decay(const void* q, const void* k, const void* v, void* o, const float* s0, float* s_out,
+                                  const float* log_decay, int B, int H, int N, int dk, int dv, la_dtype dt, int chunk,
+                                  void* workspace, size_t ws_bytes, la_stream_t stream);
+LA_API size_t la_prefill_varlen_decay_workspace_size(int n_seq, int T, int H, int dk, int dv, la_dtype dt);
+LA_API la_status la_prefill_varlen_decay(const void* q, const void* k, const void* v, void* o,
+                                         const int32_t* cu_seqlens, int n_seq, int T, const float* state_pool,
+                                         int n_pool, const int32_t* init_idx, float* s_out, const float* log_decay,
+                                         int H, int dk, int dv, la_dtype dt, int chunk, void* workspace,
+                                         size_t ws_bytes, la_stream_t stream);
+LA_API la_status la_decode_step_decay(const void* q, const void* k, const void* v, void* o, void* S,
+                                      const float* log_decay, int B, int H, int dk, int dv, la_dtype dt,
+                                      la_state_dtype sdt, la_stream_t stream);
+LA_API size_t la_prefill_decay_backward_workspace_size(int B, int H, int N, int d_k, int d_v, la_dtype dt);
+LA_API la_status la_prefill_decay_backward(const void* q, const void* k, const void* v, const void* dout,
+                                           const float* s0, const float* ds_n, const float* log_decay, void* dq,
+                                           void* dk, void* dv, float* ds0, int B, int H, int N, int d_k, int d_v,
+                                           la_dtype dt, void* workspace, size_t ws_bytes, la_stream_t stream);
+
+/* Heads of a batch in any layout: element (b, h, n, i) at
+ * data[b * stride_b + h * stride_h + n * stride_n + i] (strides in elements,
+ * each a multiple of 16 bytes; data 16-byte aligned). */
+typedef struct {
+    void* data;
+    int64_t stride_b, stride_h, stride_n;
+} la_view;
+
+/*
+ * Norm of every query and key head with the rotation by the token's position,
+ * in one pass: for each row x of d values (one head of one token)
+ *
+ *     y = R(p) (w * x * (mean_i x_i^2 + eps)^(-1/2))
+ *
+ * R(p) turns the pair (a, b) of frequency i by the angle p * inv_freq[i] to
+ * (a cos - b sin, b cos + a sin), i < rot / 2; pairs are dims (i, i + rot/2), or
+ * (2i, 2i + 1) with interleaved != 0; dims from rot on are only normed.  The
+ * angle is formed in double (positions of millions keep theirs), everything
+ * else in fp32 with one rounding to `dt`.
+ *   q, q_out: Hq heads;  k, k_out: Hk heads (either may be 0)   dtype `dt`,
+ *          d in {64, 128}, any strides that keep rows 16-byte aligned: q and k
+ *          may be slices of one projection's output, q_out and k_out the
+ *          contiguous [B, H, N, d], [T, H, d] (B = 1) or [B, H, d] (N = 1) that
+ *          the attention calls read.  Outputs must not overlap inputs.
+ *   q_weight, k_weight: [d] in `dt` or fp32 (`wdt`), 16-byte aligned.
+ *   inv_freq: fp32 [rot / 2]; rot: a multiple of 16 in [0, d] (0: norm only).
+ *   positions: int32 (pos64 = 0) or int64 (pos64 != 0), token (b, n) at
+ *          positions[b * pos_stride_b + n * pos_stride_n]; NULL: position n.
+ * All pointers but the views themselves are device pointers.  Errors:
+ * LA_ERR_INVALID_ARG (null, negative, misaligned), LA_ERR_UNSUPPORTED (d, rot,
+ * dtype), LA_ERR_CUDA (launch).
+ */
+LA_API la_status la_qk_norm_rope(const la_view* q, const la_view* k, const la_view* q_out, const la_view* k_out,
+                                 const void* q_weight, const void* k_weight, const float* inv_freq,
+                                 const void* positions, int pos64, int64_t pos_stride_b, int64_t pos_stride_n, int B,
+                                 int N, int Hq, int Hk, int d, int rot, float eps, int interleaved, la_dtype dt,
+                                 la_dtype wdt, la_stream_t stream);
+/*
+ * Its gradients: given dq_out and dk_out (same shapes as q and k, any such
+ * strides) it forms the norms again from q and k and writes dq, dk (dtype `dt`,
+ * any such strides) and dq_weight, dk_weight (fp32 [d], or NULL: not wanted).
+ * The weight gradients are summed in a fixed order.  workspace: at least
+ * la_qk_norm_rope_backward_workspace_size(d) bytes (device, 16-byte aligned).
+ */
+LA_API size_t la_qk_norm_rope_backward_workspace_size(int d);
+LA_API la_status la_qk_norm_rope_backward(const la_view* dq_out, const la_view* dk_out, const la_view* q,
+                                          const la_view* k, const void* q_weight, const void* k_weight,
+                                          const float* inv_freq, const void* positions, int pos64,
+                                          int64_t pos_stride_b, int64_t pos_stride_n, const la_view* dq,
+                                          const la_view* dk, float* dq_weight, float* dk_weight, int B, int N, int Hq,
+                                          int Hk, int d, int rot, float eps, int interleaved, la_dtype dt,
+                                          la_dtype wdt, void* workspace, size_t ws_bytes, la_stream_t stream);
+
+/*
  * Reads the device status word of the current device (synchronizes the
  * device).  *out receives LA_OK or LA_ERR_TIMEOUT; clear != 0 resets it.
  */

@@ -8,7 +8,10 @@ CUDA stream) and calls the CUDA library; all computation runs in its kernels.
 
 (page "MiniMax-M1で理解する…" (zenn.dev), section "線形アテンションの数学的基礎";
 tiled as on page "MiniMax: «Почему M2 в итоге стала моделью с полным
-вниманием?»", section 1, glossary entry "Lightning Attention").
+вниманием?»", section 1, glossary entry "Lightning Attention").  With ``log_decay`` the state decays
+between tokens, S_t = exp(log_decay[h]) S_{t-1} + k_t (x) v_t for head h.
+``qk_norm_rope`` forms the queries and keys from a projection's output: the norm
+of every head and the rotation by the token's position.
 """
 from __future__ import annotations
 
@@ -21,7 +24,7 @@ from ._abi import LAError, lib
 
 __all__ = ["prefill", "prefill_host", "prefill_varlen", "prefill_varlen_noalloc", "prefill_backward", "decode_step",
            "decode_verify",
-           "decode_commit",
+           "decode_commit", "qk_norm_rope", "qk_norm_rope_backward",
            "device_status", "LAError",
            "lib", "prefill_workspace_size", "prefill_varlen_workspace_size"]
 
@@ -60,6 +63,15 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _check_decay(log_decay: torch.Tensor, H: int, device, phi: str = "identity"):
+    """log_decay: fp32 [H] on the tensors' device, without a feature map."""
+    _need(log_decay, "log_decay", torch.float32, device)
+    if tuple(log_decay.shape) != (H,):
+        raise ValueError(f"log_decay must be [H] = [{H}], got {tuple(log_decay.shape)}")
+    if phi != "identity":
+        raise ValueError("log_decay needs phi='identity'")
+
+
 def _need_host(t: torch.Tensor, name: str, dtype=None):
     if t.device.type != "cpu":
         raise ValueError(f"{name} must be a host (CPU) tensor")
@@ -80,12 +92,14 @@ def prefill_varlen_workspace_size(n_seq: int, T: int, H: int, d: int, dtype: tor
 
 def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional[torch.Tensor] = None, *,
             chunk: int = 0, out: Optional[torch.Tensor] = None, s_out: Optional[torch.Tensor] = None,
-            return_state: bool = True, workspace: Optional[torch.Tensor] = None, phi: str = "identity"
-            ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+            return_state: bool = True, workspace: Optional[torch.Tensor] = None, phi: str = "identity",
+            log_decay: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Dense prefill over q, k, v of shape [B, H, N, d]; returns (O, S_N).
 
     s0 (fp32 [B, H, d, d]) is the state before the first token (zero if None);
-    phi ("identity", "elu1", "relu") is the feature map on q and k.
+    phi ("identity", "elu1", "relu") is the feature map on q and k.  log_decay
+    (fp32 [H], values <= 0): S_t = exp(log_decay[h]) S_{t-1} + k_t (x) v_t
+    (identity feature map only).
     """
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, n, q.dtype, q.device)
@@ -105,11 +119,20 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional[torc
         s_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
     if s_out is not None:
         _need(s_out, "s_out", torch.float32, q.device)
+    if log_decay is not None:
+        _check_decay(log_decay, H, q.device, phi)
+        if tuple(out.shape) != (B, H, N, dv) or (s_out is not None and tuple(s_out.shape) != (B, H, dk, dv)):
+            raise ValueError("out must be [B, H, N, dv] and s_out [B, H, dk, dv]")
     need = int(lib.la_prefill_workspace_size_ex(B, H, N, dk, dv, dt, _phi_code(phi)))
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     with torch.cuda.device(q.device):
+        if log_decay is not None:
+            _abi.check(lib.la_prefill_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(s0), _ptr(s_out),
+                                            _ptr(log_decay), B, H, N, dk, dv, dt, chunk, _ptr(workspace), ws_bytes,
+                                            _stream(q.device)), "la_prefill_decay")
+            return out, s_out
         _abi.check(lib.la_prefill_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(s0), _ptr(s_out),
                                      B, H, N, dk, dv, dt, chunk, _phi_code(phi), _ptr(workspace), ws_bytes,
                                      _stream(q.device)),
@@ -161,10 +184,12 @@ def prefill_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional
 
 def prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: torch.Tensor,
                      s0: Optional[torch.Tensor] = None, ds_n: Optional[torch.Tensor] = None, *,
-                     need_ds0: bool = True, workspace: Optional[torch.Tensor] = None):
+                     need_ds0: bool = True, workspace: Optional[torch.Tensor] = None,
+                     log_decay: Optional[torch.Tensor] = None):
     """Gradients of ``prefill`` for dL/dO = dout and dL/dS_N = ds_n (zero if None).
 
-    q, k, v, dout: [B, H, N, d]; s0, ds_n: fp32 [B, H, d, d] or None.
+    q, k, v, dout: [B, H, N, d]; s0, ds_n: fp32 [B, H, d, d] or None; log_decay
+    as given to ``prefill`` (a constant: it has no gradient).
     Returns (dq, dk, dv, ds0) with dq, dk, dv in the input dtype and ds0 fp32
     (None unless need_ds0).
     """
@@ -178,6 +203,8 @@ def prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: to
             _need(t, n, torch.float32, q.device)
             if tuple(t.shape) != (B, H, d, d):
                 raise ValueError(f"{n} must be [B, H, d, d]")
+    if log_decay is not None:
+        _check_decay(log_decay, H, q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds0 = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if need_ds0 else None
     need = int(lib.la_prefill_backward_workspace_size(B, H, N, d, d, _dtype_code(q)))
@@ -185,6 +212,12 @@ def prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: to
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     with torch.cuda.device(q.device):
+        if log_decay is not None:
+            _abi.check(lib.la_prefill_decay_backward(
+                _ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(s0), _ptr(ds_n), _ptr(log_decay), _ptr(dq), _ptr(dk),
+                _ptr(dv), _ptr(ds0), B, H, N, d, d, _dtype_code(q), _ptr(workspace), ws_bytes, _stream(q.device)),
+                "la_prefill_decay_backward")
+            return dq, dk, dv, ds0
         _abi.check(lib.la_prefill_backward_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(s0), _ptr(ds_n), _ptr(dq),
                                               _ptr(dk), _ptr(dv), _ptr(ds0), B, H, N, d, d, _dtype_code(q),
                                               _ptr(workspace), ws_bytes, _stream(q.device)), "la_prefill_backward_ex")
@@ -229,15 +262,19 @@ def _check_packed(q, k, v, cu_seqlens, state_pool, init_idx, out, s_out):
 def prefill_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
                    state_pool: Optional[torch.Tensor] = None, init_idx: Optional[torch.Tensor] = None, *,
                    chunk: int = 0, out: Optional[torch.Tensor] = None, s_out: Optional[torch.Tensor] = None,
-                   return_state: bool = True, workspace: Optional[torch.Tensor] = None, phi: str = "identity"
-                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                   return_state: bool = True, workspace: Optional[torch.Tensor] = None, phi: str = "identity",
+                   log_decay: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Packed ragged prefill: q, k [T, H, d], v [T, H, d], cu_seqlens int32 [n_seq + 1].
 
     Sequence n starts from state_pool[init_idx[n]] when init_idx[n] >= 0;
-    phi is the feature map on q and k.  Returns (O [T, H, d], S [n_seq, H, d, d]).
+    phi is the feature map on q and k, log_decay (fp32 [H], <= 0) the decay per
+    head (identity feature map only).  Returns (O [T, H, d], S [n_seq, H, d, d]);
+    rows of O behind the last sequence are left as they were.
     """
     T, H, dk, dv, n_seq, n_pool = _check_packed(q, k, v, cu_seqlens, state_pool, init_idx, out, s_out)
     dt = _dtype_code(q)
+    if log_decay is not None:
+        _check_decay(log_decay, H, q.device, phi)
     if out is None:
         out = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
     if s_out is None and return_state:
@@ -247,6 +284,12 @@ def prefill_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     with torch.cuda.device(q.device):
+        if log_decay is not None:
+            _abi.check(lib.la_prefill_varlen_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(cu_seqlens), n_seq, T,
+                                                   _ptr(state_pool), n_pool, _ptr(init_idx), _ptr(s_out),
+                                                   _ptr(log_decay), H, dk, dv, dt, chunk, _ptr(workspace), ws_bytes,
+                                                   _stream(q.device)), "la_prefill_varlen_decay")
+            return out, s_out
         _abi.check(lib.la_prefill_varlen_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(cu_seqlens), n_seq, T,
                                             _ptr(state_pool), n_pool, _ptr(init_idx), _ptr(s_out), H, dk, dv, dt,
                                             chunk, _phi_code(phi), _ptr(workspace), ws_bytes, _stream(q.device)),
@@ -282,8 +325,12 @@ _STATE_DT = {torch.float32: _abi.LA_STATE_FP32, torch.bfloat16: _abi.LA_STATE_BF
 
 
 def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, S: torch.Tensor, *,
-                out: Optional[torch.Tensor] = None, phi: str = "identity") -> torch.Tensor:
+                out: Optional[torch.Tensor] = None, phi: str = "identity",
+                log_decay: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token per (batch, head): S <- S + k (x) v in place, returns o = q S.
+
+    With log_decay (fp32 [H], values <= 0; identity feature map only)
+    S <- exp(log_decay[h]) S + k (x) v.
 
     q, k, v: [B, H, d]; S: [B, H, d, d] in fp32, or in bf16 / fp16 /
     float8_e4m3fn / float8_e5m2 (state stored in low precision, updated in fp32
@@ -304,6 +351,15 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, S: torch.Tens
     if out is None:
         out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
     _need(out, "out", q.dtype, q.device)
+    if log_decay is not None:
+        _check_decay(log_decay, H, q.device, phi)
+        if tuple(out.shape) != (B, H, dv):
+            raise ValueError("out must be [B, H, dv]")
+        with torch.cuda.device(q.device):
+            _abi.check(lib.la_decode_step_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(S), _ptr(log_decay), B, H,
+                                                dk, dv, _dtype_code(q), _STATE_DT[S.dtype], _stream(q.device)),
+                       "la_decode_step_decay")
+        return out
     with torch.cuda.device(q.device):
         _abi.check(lib.la_decode_step_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(S), B, H, dk, dv,
                                          _dtype_code(q), _STATE_DT[S.dtype], _phi_code(phi), _stream(q.device)),
@@ -353,6 +409,129 @@ def decode_commit(k: torch.Tensor, v: torch.Tensor, S: torch.Tensor, accepted: t
     with torch.cuda.device(k.device):
         _abi.check(lib.la_decode_commit(_ptr(k), _ptr(v), _ptr(S), _ptr(accepted), B, H, m, dk, dv,
                                         _dtype_code(k), _phi_code(phi), _stream(k.device)), "la_decode_commit")
+
+
+def _heads_view(t: torch.Tensor, name: str, dtype, device):
+    """la_view of heads [B, H, N, d] or packed [T, H, d] (one batch entry), last dim contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of a dimension of one entry (or none) says nothing
+    st = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
+    b, h, n = st if t.dim() == 4 else (0, st[1], st[0])
+    return _abi.View(t.data_ptr(), b, h, n)
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions):
+    """Checks of the arguments that both directions share; returns (B, N, Hq, Hk, d, positions' pointer, their
+    width, strides, the weights' dtype code)."""
+    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must be [B, H, N, d], or packed [T, H, d]")
+    if q.dim() == 4:
+        B, Hq, N, d = q.shape
+        Hk, same = k.shape[1], k.shape[0] == B and k.shape[2] == N
+    else:
+        N, Hq, d = q.shape
+        B, Hk, same = 1, k.shape[1], k.shape[0] == N
+    if not same:
+        raise ValueError("q and k must have the same tokens")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _need(t, n, None, q.device)
+        if tuple(t.shape) != (d,):
+            raise ValueError(f"{n} must be [d] = [{d}], got {tuple(t.shape)}")
+    if q_weight.dtype != k_weight.dtype or q_weight.dtype not in (torch.float32, q.dtype):
+        raise TypeError("q_weight and k_weight must both be float32, or both of q's dtype")
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, q.device)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot / 2]")
+        rot = 2 * inv_freq.numel()
+    pos64, psb, psn = 0, 0, 0
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+        if positions.device != q.device:
+            raise ValueError(f"positions is on {positions.device}, expected {q.device}")
+        pos64 = int(positions.dtype == torch.int64)
+        if q.dim() == 4 and tuple(positions.shape) == (B, N):
+            psb, psn = positions.stride()
+        elif tuple(positions.shape) == (N,):
+            psn = positions.stride(0)
+        else:
+            raise ValueError("positions must be [B, N] or [N] for [B, H, N, d], [T] for [T, H, d]")
+    elif q.dim() == 3 and rot:
+        raise ValueError("packed q and k need positions")
+    return B, N, Hq, Hk, d, rot, pos64, psb, psn, _DT[q_weight.dtype]
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                 inv_freq: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, *,
+                 eps: float = 1e-6, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Norm of every query and key head and rotation by the token's position.
+
+    Each row x of d values becomes R(p) (w * x / sqrt(mean(x^2) + eps)): R turns
+    the pairs (i, i + rot/2) -- (2i, 2i + 1) if interleaved -- of the first
+    rot = 2 len(inv_freq) dims by the angle p * inv_freq[i] (norm only if
+    inv_freq is None).  q [B, Hq, N, d] and k [B, Hk, N, d], or packed [T, H, d]
+    (also one decode token of each sequence), of any strides with a contiguous
+    last dim, e.g. slices of one projection's output; weights [d] in fp32 or q's
+    dtype; inv_freq fp32; positions int32 / int64 [B, N] or [N] (default
+    0 .. N-1), [T] for packed.  Returns contiguous (q_out, k_out), or writes the
+    given ones (any strides).
+    """
+    dt = _dtype_code(q)
+    B, N, Hq, Hk, d, rot, pos64, psb, psn, wdt = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    views = [_heads_view(t, n, q.dtype, q.device)
+             for t, n in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))]
+    with torch.cuda.device(q.device):
+        _abi.check(lib.la_qk_norm_rope(*views, _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), pos64,
+                                       psb, psn, B, N, Hq, Hk, d, rot, eps, int(interleaved), dt, wdt,
+                                       _stream(q.device)), "la_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                          q_weight: torch.Tensor, k_weight: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
+                          positions: Optional[torch.Tensor] = None, *, eps: float = 1e-6, interleaved: bool = False,
+                          dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``qk_norm_rope`` for dL/dq_out and dL/dk_out.
+
+    q, k, weights, inv_freq, positions, eps and interleaved as in the forward
+    call.  Returns (dq, dk, dq_weight, dk_weight): dq and dk in q's dtype
+    (contiguous, or the given ones of any strides), the weight gradients fp32.
+    """
+    dt = _dtype_code(q)
+    B, N, Hq, Hk, d, rot, pos64, psb, psn, wdt = _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dk is None else dk
+    for t, x, n in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out"), (dq, q, "dq"), (dk, k, "dk")):
+        if t.shape != x.shape:
+            raise ValueError(f"{n} must be {tuple(x.shape)}, got {tuple(t.shape)}")
+    views = [_heads_view(t, n, q.dtype, q.device) for t, n in
+             ((dq_out, "dq_out"), (dk_out, "dk_out"), (q, "q"), (k, "k"), (dq, "dq"), (dk, "dk"))]
+    dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
+    with torch.cuda.device(q.device):
+        need = int(lib.la_qk_norm_rope_backward_workspace_size(d))
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_bytes = workspace.numel() * workspace.element_size()
+        _abi.check(lib.la_qk_norm_rope_backward(*views[:4], _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                                                _ptr(positions), pos64, psb, psn, *views[4:], _ptr(dqw), _ptr(dkw), B,
+                                                N, Hq, Hk, d, rot, eps, int(interleaved), dt, wdt, _ptr(workspace),
+                                                ws_bytes, _stream(q.device)), "la_qk_norm_rope_backward")
+    return dq, dk, dqw, dkw
 
 
 def device_status(clear: bool = True) -> int:

@@ -27,10 +27,20 @@ LA_PHI_IDENTITY = 0
 LA_PHI_ELU1 = 1
 LA_PHI_RELU = 2
 
+class View(ctypes.Structure):
+    """la_view of include/la.h: data pointer and strides (elements) of [B, H, N, d] heads."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
 # name -> (restype, argtypes), mirroring include/la.h
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_l = ctypes.c_int64
+_f = ctypes.c_float
+_view = ctypes.POINTER(View)
 SIGNATURES = {
     "la_status_string": (ctypes.c_char_p, [_i]),
     "la_last_error": (ctypes.c_char_p, []),
@@ -55,6 +65,20 @@ SIGNATURES = {
     "la_prefill_backward_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "la_prefill_backward_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz,
                                     _vp]),
+    "la_prefill_decay_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "la_prefill_decay": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "la_prefill_varlen_decay_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "la_prefill_varlen_decay": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                                     _sz, _vp]),
+    "la_decode_step_decay": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+    "la_prefill_decay_backward_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "la_prefill_decay_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                       _vp, _sz, _vp]),
+    "la_qk_norm_rope": (_i, [_view, _view, _view, _view, _vp, _vp, _vp, _vp, _i, _l, _l, _i, _i, _i, _i, _i, _i, _f, _i,
+                             _i, _i, _vp]),
+    "la_qk_norm_rope_backward_workspace_size": (_sz, [_i]),
+    "la_qk_norm_rope_backward": (_i, [_view, _view, _view, _view, _vp, _vp, _vp, _vp, _i, _l, _l, _view, _view, _vp,
+                                      _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _i, _vp, _sz, _vp]),
     "la_device_status": (_i, [ctypes.POINTER(_i), _i]),
     "la_selftest_wait_timeout": (_i, [_i, _vp]),
     "la_prefill_varlen_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp]),

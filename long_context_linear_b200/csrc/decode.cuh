@@ -16,10 +16,17 @@
 // format to nearest even (the 8-bit formats saturate at their largest finite
 // value); o uses the stored (rounded) state.  A feature map
 // phi (phi.cuh) is applied to q and k as they are loaded.
+//
+// kDecay: S <- lam S + k v^T with a decay per head (decay.cuh); lam is held as
+// two fp32 values (one alone is up to 3e-8 off at every token: 3e-4 over a
+// memory of 10^4 tokens) and lam S is rounded to fp32 before the fused
+// multiply-add of k v.  Two more operations per element in a kernel bound by
+// the state's bytes.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include "decay.cuh"
 #include "phi.cuh"
 
 namespace lcl {
@@ -142,10 +149,10 @@ __host__ __device__ constexpr int decode_min_blocks() {
     return Vec<SS>::E == 16 ? 8 : (Vec<SS>::E == 8 ? 5 : 3);
 }
 
-template <typename T, typename SS, int D>
+template <typename T, typename SS, int D, bool kDecay = false>
 __global__ void __launch_bounds__(decode_threads<SS>(), decode_min_blocks<SS>())
 decode_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, T* __restrict__ o,
-                   SS* __restrict__ S, int phi) {
+                   SS* __restrict__ S, int phi, const float* __restrict__ log_decay = nullptr, int H = 1) {
     constexpr int NT = decode_threads<SS>();
     constexpr int E = Vec<SS>::E;          // state values per 16-byte vector
     constexpr int TPR = D / E;             // threads per row
@@ -154,6 +161,7 @@ decode_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     static_assert(TPR * RS == NT && RS * RPT == D, "thread layout must cover the state exactly");
     __shared__ float qs[D], ks[D], vs[D];
     __shared__ float red[RS][D];
+    __shared__ float2 lam_s;
 
     const long u = blockIdx.x;
     const int tid = threadIdx.x;
@@ -169,7 +177,15 @@ decode_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         ks[e] = apply_phi(ld_f(k + u * D + e), phi);
         vs[e] = ld_f(v + u * D + e);
     }
+    if constexpr (kDecay) {
+        if (tid == NT - 1) decay::power2(log_decay[blockIdx.x % H], 1, lam_s.x, lam_s.y);
+    }
     __syncthreads();
+    float lh = 1.f, ll = 0.f;
+    if constexpr (kDecay) {
+        lh = lam_s.x;
+        ll = lam_s.y;
+    }
     float vj[E], acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -183,7 +199,7 @@ decode_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         float y[E];
         Vec<SS>::unpack(x[m], y);
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = fmaf(ki, vj[e], y[e]);
+        for (int e = 0; e < E; ++e) y[e] = fmaf(ki, vj[e], kDecay ? fmaf(y[e], lh, y[e] * ll) : y[e]);
         __stcs(&Su[i * TPR + cv], Vec<SS>::pack(y));
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(qi, y[e], acc[e]);

@@ -15,6 +15,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "la.h"
@@ -28,6 +29,7 @@
 #include "seg_prefix.cuh"
 #include "decode_multi.cuh"
 #include "phi_map.cuh"
+#include "norm_rope.cuh"
 
 namespace lcl {
 
@@ -74,19 +76,19 @@ std::mutex g_dev_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-template <typename T>
+template <typename T, bool kDecay>
 cudaError_t set_simt_attrs() {
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 128, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  simt::smem_bytes<128, 64>())) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 128, 64, kDecay>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, simt::smem_bytes<128, 64>())) != cudaSuccess)
         return e;
-    if ((e = cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 128, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  simt::smem_bytes<128, 32>())) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 128, 32, kDecay>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, simt::smem_bytes<128, 32>())) != cudaSuccess)
         return e;
-    if ((e = cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 64, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  simt::smem_bytes<64, 64>())) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 64, 64, kDecay>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, simt::smem_bytes<64, 64>())) != cudaSuccess)
         return e;
-    return cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 64, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(simt::prefill_simt_kernel<T, 64, 32, kDecay>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 simt::smem_bytes<64, 32>());
 }
 
@@ -157,7 +159,9 @@ la_status device_info(DeviceInfo** out) {
         if ((e = cudaFuncSetAttribute(dmulti::verify_tf32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       dmulti::vtf::SMEM_BYTES)) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(verify_tf32)");
-        if ((e = set_simt_attrs<float>()) != cudaSuccess || (e = set_simt_attrs<__nv_bfloat16>()) != cudaSuccess)
+        if ((e = set_simt_attrs<float, false>()) != cudaSuccess ||
+            (e = set_simt_attrs<__nv_bfloat16, false>()) != cudaSuccess ||
+            (e = set_simt_attrs<float, true>()) != cudaSuccess || (e = set_simt_attrs<__nv_bfloat16, true>()) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(prefill_simt)");
         const unsigned long long id = current_ctx_id();
         if (id != d.ctx) d.h2d = d.d2h = nullptr;  // copy streams of a context that is gone
@@ -318,15 +322,21 @@ la_status launch_wide(int grid, const CUtensorMap& mq, const CUtensorMap& mk, co
     return after_launch(what);
 }
 
+template <typename T, int D, bool kDecay>
+void launch_simt_dd(int cs, int grid, const void* q, const void* k, const void* v, void* o, const simt::Params& sp,
+                    cudaStream_t st) {
+    if (cs == 32)
+        simt::prefill_simt_kernel<T, D, 32, kDecay><<<grid, simt::NUM_THREADS, simt::smem_bytes<D, 32>(), st>>>(
+            (const T*)q, (const T*)k, (const T*)v, (T*)o, sp);
+    else
+        simt::prefill_simt_kernel<T, D, 64, kDecay><<<grid, simt::NUM_THREADS, simt::smem_bytes<D, 64>(), st>>>(
+            (const T*)q, (const T*)k, (const T*)v, (T*)o, sp);
+}
 template <typename T, int D>
 void launch_simt_d(int cs, int grid, const void* q, const void* k, const void* v, void* o, const simt::Params& sp,
                    cudaStream_t st) {
-    if (cs == 32)
-        simt::prefill_simt_kernel<T, D, 32><<<grid, simt::NUM_THREADS, simt::smem_bytes<D, 32>(), st>>>(
-            (const T*)q, (const T*)k, (const T*)v, (T*)o, sp);
-    else
-        simt::prefill_simt_kernel<T, D, 64><<<grid, simt::NUM_THREADS, simt::smem_bytes<D, 64>(), st>>>(
-            (const T*)q, (const T*)k, (const T*)v, (T*)o, sp);
+    if (sp.log_decay) launch_simt_dd<T, D, true>(cs, grid, q, k, v, o, sp, st);
+    else launch_simt_dd<T, D, false>(cs, grid, q, k, v, o, sp, st);
 }
 
 template <typename T>
@@ -344,15 +354,21 @@ la_status launch_simt(int d, int chunk, int grid, const void* q, const void* k, 
 
 namespace lcl {
 namespace {
+template <typename T, typename SS, bool kDecay>
+void launch_decode_d(int dk, int grid, const void* q, const void* k, const void* v, void* o, void* S, int phi,
+                     const float* log_decay, int H, cudaStream_t st) {
+    if (dk == 128)
+        dec::decode_step_kernel<T, SS, 128, kDecay><<<grid, dec::decode_threads<SS>(), 0, st>>>(
+            (const T*)q, (const T*)k, (const T*)v, (T*)o, (SS*)S, phi, log_decay, H);
+    else
+        dec::decode_step_kernel<T, SS, 64, kDecay><<<grid, dec::decode_threads<SS>(), 0, st>>>(
+            (const T*)q, (const T*)k, (const T*)v, (T*)o, (SS*)S, phi, log_decay, H);
+}
 template <typename T, typename SS>
 void launch_decode(int dk, int grid, const void* q, const void* k, const void* v, void* o, void* S, int phi,
-                   cudaStream_t st) {
-    if (dk == 128)
-        dec::decode_step_kernel<T, SS, 128><<<grid, dec::decode_threads<SS>(), 0, st>>>(
-            (const T*)q, (const T*)k, (const T*)v, (T*)o, (SS*)S, phi);
-    else
-        dec::decode_step_kernel<T, SS, 64><<<grid, dec::decode_threads<SS>(), 0, st>>>(
-            (const T*)q, (const T*)k, (const T*)v, (T*)o, (SS*)S, phi);
+                   const float* log_decay, int H, cudaStream_t st) {
+    if (log_decay) launch_decode_d<T, SS, true>(dk, grid, q, k, v, o, S, phi, log_decay, H, st);
+    else launch_decode_d<T, SS, false>(dk, grid, q, k, v, o, S, phi, nullptr, 1, st);
 }
 }  // namespace
 }  // namespace lcl
@@ -499,6 +515,56 @@ la_status phi_prepass(const void** q, const void** k, void* scratch, long elems,
 
 }  // namespace
 
+namespace {
+
+// Log decays: a device array of H fp32 values, <= 0 and not NaN.  Their values
+// are a precondition, checked (with a copy and a stream sync) under LA_VALIDATE=1.
+la_status check_log_decay(const float* log_decay, int H, cudaStream_t st) {
+    if (!log_decay) return fail(LA_ERR_INVALID_ARG, "log_decay must be non-null");
+    if (reinterpret_cast<uintptr_t>(log_decay) & 3u) return fail(LA_ERR_INVALID_ARG, "log_decay must be 4-byte aligned");
+    if (!env_validate() || H <= 0) return LA_OK;
+    std::vector<float> g(H);
+    cudaError_t e = cudaMemcpyAsync(g.data(), log_decay, sizeof(float) * H, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return cuda_fail(e, "LA_VALIDATE copy of log_decay");
+    for (int h = 0; h < H; ++h)
+        if (!(g[h] <= 0.f)) return fail(LA_ERR_INVALID_ARG, "log_decay[%d] = %g is not <= 0", h, (double)g[h]);
+    return LA_OK;
+}
+
+// States before every segment of a dense batch (seg_prefix.cuh).
+la_status launch_seg_prefix(const float* sums, const float* init, float* starts, long U, int P, int d, bool reverse,
+                            bool init_t, const float* log_decay, int H, int seg_len, int N, DeviceInfo* di,
+                            cudaStream_t st) {
+    const long threads = U * (long)(d * d / 4);
+    const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 4L * di->sms);
+    if (log_decay)
+        segp::seg_prefix_kernel<true><<<blocks, segp::NUM_THREADS, 0, st>>>(
+            sums, init, starts, U, P, d * d, reverse ? 1 : 0, init_t ? 1 : 0, d, log_decay, H, seg_len,
+            N - (P - 1) * seg_len);
+    else
+        segp::seg_prefix_kernel<false><<<blocks, segp::NUM_THREADS, 0, st>>>(sums, init, starts, U, P, d * d,
+                                                                            reverse ? 1 : 0, init_t ? 1 : 0, d);
+    return after_launch("segment prefix launch");
+}
+
+// The same for a packed batch.
+la_status launch_seg_prefix_varlen(const float* sums, const float* pool, const int* init_idx, const int* order,
+                                   const int* seg_off, const int* seg_off_nl, float* starts, int n_seq, int H, int d,
+                                   const float* log_decay, const int* seg_len, DeviceInfo* di, cudaStream_t st) {
+    const long threads = (long)n_seq * H * (d * d / 4);
+    const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 4L * di->sms);
+    if (log_decay)
+        segp::seg_prefix_varlen_kernel<true><<<blocks, segp::NUM_THREADS, 0, st>>>(
+            sums, pool, init_idx, order, seg_off, seg_off_nl, starts, n_seq, H, d * d, log_decay, seg_len);
+    else
+        segp::seg_prefix_varlen_kernel<false><<<blocks, segp::NUM_THREADS, 0, st>>>(
+            sums, pool, init_idx, order, seg_off, seg_off_nl, starts, n_seq, H, d * d);
+    return after_launch("varlen segment prefix launch");
+}
+
+}  // namespace
+
 // The FFMA prefill over dense units.  When the units fill less than half of
 // the SMs and the workspace holds segment_workspace_bytes(U, P, d, d), each
 // unit's sequence is cut into P segments: a state-only pass sums K^T V per
@@ -506,7 +572,7 @@ la_status phi_prepass(const void** q, const void** k, void* scratch, long elems,
 // segment's starting state from them and `init`, and the main pass runs all
 // segments at once.  Otherwise one CTA runs each unit whole.
 la_status simt_dense(const void* q, const void* k, const void* v, void* o, const float* init, bool init_t,
-                     float* s_out, bool reverse, la_phi phi, long U, int N, int d, la_dtype dt, int chunk,
+                     float* s_out, bool reverse, la_phi phi, const float* log_decay, int H, long U, int N, int d, la_dtype dt, int chunk,
                      DeviceInfo* di, void* ws, size_t ws_bytes, cudaStream_t st) {
     simt::Params sp{};
     sp.mode = 0;
@@ -516,6 +582,8 @@ la_status simt_dense(const void* q, const void* k, const void* v, void* o, const
     sp.phi = phi;
     sp.reverse = reverse ? 1 : 0;
     sp.init_transposed = init_t ? 1 : 0;
+    sp.log_decay = log_decay;
+    sp.heads = H;
     auto go = [&](const simt::Params& x, long grid) {
         return dt == LA_FP32 ? launch_simt<float>(d, chunk, (int)grid, q, k, v, o, x, st)
                              : launch_simt<__nv_bfloat16>(d, chunk, (int)grid, q, k, v, o, x, st);
@@ -538,11 +606,8 @@ la_status simt_dense(const void* q, const void* k, const void* v, void* o, const
     p1.state_only = 1;
     la_status s;
     if ((s = go(p1, U * (P - 1))) != LA_OK) return s;
-    const long threads = U * (long)(d * d / 4);
-    const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 4L * di->sms);
-    segp::seg_prefix_kernel<<<blocks, segp::NUM_THREADS, 0, st>>>(sums, init, starts, U, P, d * d, reverse ? 1 : 0,
-                                                                 init_t ? 1 : 0, d);
-    if ((s = after_launch("segment prefix launch")) != LA_OK) return s;
+    if ((s = launch_seg_prefix(sums, init, starts, U, P, d, reverse, init_t, log_decay, H, seg_len, N, di, st)) != LA_OK)
+        return s;
     sp.n_seg = P;
     sp.seg_len = seg_len;
     sp.seg_init = starts;
@@ -575,9 +640,11 @@ la_status la_prefill(const void* q, const void* k, const void* v, void* o, const
                          stream);
 }
 
-la_status la_prefill_ex(const void* q, const void* k, const void* v, void* o, const float* s0, float* s_out, int B,
-                        int H, int N, int dk, int dv, la_dtype dt, int chunk, la_phi phi, void* workspace,
-                        size_t ws_bytes, la_stream_t stream) {
+// la_prefill_ex, and la_prefill_decay with a log_decay (phi: identity)
+static la_status prefill_dense(const void* q, const void* k, const void* v, void* o, const float* s0, float* s_out,
+                               int B, int H, int N, int dk, int dv, la_dtype dt, int chunk, la_phi phi,
+                               bool decayed, const float* log_decay, void* workspace, size_t ws_bytes,
+                               la_stream_t stream) {
     g_last_error[0] = 0;
     la_status s = check_dims(dk, dv, dt);
     if (s != LA_OK) return s;
@@ -589,14 +656,17 @@ la_status la_prefill_ex(const void* q, const void* k, const void* v, void* o, co
     if (N > 0 && (!q || !k || !v || !o)) return fail(LA_ERR_INVALID_ARG, "q, k, v, o must be non-null");
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(s0) || !aligned16(s_out))
         return fail(LA_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
-    const bool tcpath = tensor_core_path(dk, dt, chunk);
+    const bool tcpath = tensor_core_path(dk, dt, chunk) && !decayed;
     if ((s = check_chunk(chunk, tcpath)) != LA_OK) return s;
+    if (decayed && !log_decay) return fail(LA_ERR_INVALID_ARG, "log_decay must be non-null");
     DeviceInfo* di;
     if ((s = device_info(&di)) != LA_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (decayed && (s = check_log_decay(log_decay, H, st)) != LA_OK) return s;
 
     if (!tcpath)
-        return simt_dense(q, k, v, o, s0, false, s_out, false, phi, U, N, dk, dt, chunk, di, workspace, ws_bytes, st);
+        return simt_dense(q, k, v, o, s0, false, s_out, false, phi, log_decay, H, U, N, dk, dt, chunk, di, workspace,
+                          ws_bytes, st);
 
     const int nvs = tc_slices(dv);
     tc::Params p{};
@@ -612,8 +682,9 @@ la_status la_prefill_ex(const void* q, const void* k, const void* v, void* o, co
     p.status = di->status;
     p.n_seg = 1;
     p.phi = phi;
+    p.log_decay = log_decay;
     if (N == 0 && !s_out) return LA_OK;
-    const bool wide = use_wide(U, dk, di);
+    const bool wide = !decayed && use_wide(U, dk, di);
     int seg_len;
     int P = wide ? 1 : plan_segments(U, N, tc_slices(dk), di->sms, &seg_len);
     p.seg_len = seg_len;
@@ -661,10 +732,9 @@ la_status la_prefill_ex(const void* q, const void* k, const void* v, void* o, co
         if ((s = launch_tc(std::min(p1.n_items, di->sms), mq, mk, mv, mo, p1, st, "prefill_tc (segment sums) launch")) !=
             LA_OK)
             return s;
-        const long threads = U * (long)(dk * dv / 4);
-        const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 4L * di->sms);
-        segp::seg_prefix_kernel<<<blocks, segp::NUM_THREADS, 0, st>>>(seg_sums, s0, starts, U, P, dk * dv, 0, 0, dk);
-        if ((s = after_launch("segment prefix launch")) != LA_OK) return s;
+        if ((s = launch_seg_prefix(seg_sums, s0, starts, U, P, dk, false, false, log_decay, H, p.seg_len, N, di, st)) !=
+            LA_OK)
+            return s;
         p.n_seg = P;
         p.n_items = (int)(U * P * nvs);
         p.seg_init = starts;
@@ -675,6 +745,24 @@ la_status la_prefill_ex(const void* q, const void* k, const void* v, void* o, co
     }
     const int grid = std::min(p.n_items, di->sms);
     return launch_tc(grid, mq, mk, mv, mo, p, st, "prefill_tc launch");
+}
+
+la_status la_prefill_ex(const void* q, const void* k, const void* v, void* o, const float* s0, float* s_out, int B,
+                        int H, int N, int dk, int dv, la_dtype dt, int chunk, la_phi phi, void* workspace,
+                        size_t ws_bytes, la_stream_t stream) {
+    return prefill_dense(q, k, v, o, s0, s_out, B, H, N, dk, dv, dt, chunk, phi, false, nullptr, workspace, ws_bytes,
+                         stream);
+}
+
+size_t la_prefill_decay_workspace_size(int B, int H, int N, int dk, int dv, la_dtype dt) {
+    return la_prefill_workspace_size_ex(B, H, N, dk, dv, dt, LA_PHI_IDENTITY);
+}
+
+la_status la_prefill_decay(const void* q, const void* k, const void* v, void* o, const float* s0, float* s_out,
+                           const float* log_decay, int B, int H, int N, int dk, int dv, la_dtype dt, int chunk,
+                           void* workspace, size_t ws_bytes, la_stream_t stream) {
+    return prefill_dense(q, k, v, o, s0, s_out, B, H, N, dk, dv, dt, chunk, LA_PHI_IDENTITY, true, log_decay, workspace,
+                         ws_bytes, stream);
 }
 
 namespace {
@@ -745,10 +833,11 @@ la_status la_prefill_varlen(const void* q, const void* k, const void* v, void* o
                                 chunk, LA_PHI_IDENTITY, workspace, ws_bytes, stream);
 }
 
-la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void* o, const int32_t* cu_seqlens,
-                               int n_seq, int T, const float* state_pool, int n_pool, const int32_t* init_idx,
-                               float* s_out, int H, int dk, int dv, la_dtype dt, int chunk, la_phi phi,
-                               void* workspace, size_t ws_bytes, la_stream_t stream) {
+// la_prefill_varlen_ex, and la_prefill_varlen_decay with a log_decay (phi: identity)
+static la_status prefill_packed(const void* q, const void* k, const void* v, void* o, const int32_t* cu_seqlens,
+                                int n_seq, int T, const float* state_pool, int n_pool, const int32_t* init_idx,
+                                float* s_out, int H, int dk, int dv, la_dtype dt, int chunk, la_phi phi, bool decayed,
+                                const float* log_decay, void* workspace, size_t ws_bytes, la_stream_t stream) {
     g_last_error[0] = 0;
     la_status s = check_dims(dk, dv, dt);
     if (s != LA_OK) return s;
@@ -765,14 +854,16 @@ la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void
         (reinterpret_cast<uintptr_t>(init_idx) & 3u))
         return fail(LA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned, index arrays 4-byte aligned");
     if ((long)T * H > (1L << 40) || (long)n_seq * H > (1L << 30)) return fail(LA_ERR_INVALID_ARG, "problem too large");
-    const bool tcpath = tensor_core_path(dk, dt, chunk);
+    const bool tcpath = tensor_core_path(dk, dt, chunk) && !decayed;
     if ((s = check_chunk(chunk, tcpath)) != LA_OK) return s;
     const size_t need = varlen_order_bytes(n_seq);
     if (tcpath && (ws_bytes < need || !workspace || !aligned16(workspace)))
         return fail(LA_ERR_INVALID_ARG, "workspace of %zu bytes (16-byte aligned) required, got %zu", need, ws_bytes);
+    if (decayed && !log_decay) return fail(LA_ERR_INVALID_ARG, "log_decay must be non-null");
     DeviceInfo* di;
     if ((s = device_info(&di)) != LA_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (decayed && (s = check_log_decay(log_decay, H, st)) != LA_OK) return s;
 
     if (env_validate()) {
         std::vector<int32_t> cu(n_seq + 1), idx;
@@ -795,7 +886,7 @@ la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void
     if (!tcpath) {
         simt::Params sp{};
         sp.mode = 1; sp.H = H; sp.cu_seqlens = cu_seqlens; sp.pool = state_pool; sp.init_idx = init_idx;
-        sp.s_out = s_out; sp.phi = phi;
+        sp.s_out = s_out; sp.phi = phi; sp.log_decay = log_decay;
         auto go = [&](const simt::Params& x, long grid) {
             return dt == LA_FP32 ? launch_simt<float>(dk, chunk, (int)grid, q, k, v, o, x, st)
                                  : launch_simt<__nv_bfloat16>(dk, chunk, (int)grid, q, k, v, o, x, st);
@@ -833,11 +924,9 @@ la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void
             p1.init_idx = nullptr;
             if ((s = go(p1, max_nl * H)) != LA_OK) return s;
         }
-        const long threads = (long)n_seq * H * (dk * dv / 4);
-        const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 4L * di->sms);
-        segp::seg_prefix_varlen_kernel<<<blocks, segp::NUM_THREADS, 0, st>>>(sums, state_pool, init_idx, order, seg_off,
-                                                                            seg_off_nl, starts, n_seq, H, dk * dv);
-        if ((s = after_launch("varlen segment prefix launch")) != LA_OK) return s;
+        if ((s = launch_seg_prefix_varlen(sums, state_pool, init_idx, order, seg_off, seg_off_nl, starts, n_seq, H, dk,
+                                          log_decay, seg_len, di, st)) != LA_OK)
+            return s;
         sp.seg_init = starts;
         return go(sp, max_segs * H);
     }
@@ -856,7 +945,7 @@ la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void
         off_seg += ws_phi;
     }
     const int nvs = tc_slices(dv);
-    const bool wide = use_wide((long)n_seq * H, dk, di);
+    const bool wide = !decayed && use_wide((long)n_seq * H, dk, di);
     int min_seg;
     long max_segs = wide ? 0 : plan_varlen_segments(n_seq, T, H, nvs, di->sms, &min_seg);
     if (max_segs && (ws_bytes < off_seg + varlen_segment_bytes(n_seq, max_segs, H, dk) ||
@@ -879,6 +968,7 @@ la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void
     p.s_out = s_out;
     p.o = reinterpret_cast<__nv_bfloat16*>(o);
     p.status = di->status;
+    p.log_decay = log_decay;
     CUtensorMap mq, mk, mv, mo;
     const uint64_t Tm = T > 0 ? (uint64_t)T : 1;
     const uint64_t head = (uint64_t)dk * 2, tok = (uint64_t)H * dk * 2;
@@ -916,11 +1006,9 @@ la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void
                                "prefill_tc (varlen segment sums) launch")) != LA_OK)
                 return s;
         }
-        const long threads = (long)n_seq * H * (dk * dv / 4);
-        const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 4L * di->sms);
-        segp::seg_prefix_varlen_kernel<<<blocks, segp::NUM_THREADS, 0, st>>>(sums, state_pool, init_idx, order, seg_off,
-                                                                            seg_off_nl, starts, n_seq, H, dk * dv);
-        if ((s = after_launch("varlen segment prefix launch")) != LA_OK) return s;
+        if ((s = launch_seg_prefix_varlen(sums, state_pool, init_idx, order, seg_off, seg_off_nl, starts, n_seq, H, dk,
+                                          log_decay, seg_len, di, st)) != LA_OK)
+            return s;
         p.n_items = (int)(max_segs * H * nvs);
         p.seg_init = starts;
     }
@@ -932,8 +1020,30 @@ la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void
     return launch_tc(grid, mq, mk, mv, mo, p, st, "prefill_tc (varlen) launch");
 }
 
-la_status la_decode_step_ex(const void* q, const void* k, const void* v, void* o, void* S, int B, int H, int dk,
-                            int dv, la_dtype dt, la_state_dtype sdt, la_phi phi, la_stream_t stream) {
+la_status la_prefill_varlen_ex(const void* q, const void* k, const void* v, void* o, const int32_t* cu_seqlens,
+                               int n_seq, int T, const float* state_pool, int n_pool, const int32_t* init_idx,
+                               float* s_out, int H, int dk, int dv, la_dtype dt, int chunk, la_phi phi,
+                               void* workspace, size_t ws_bytes, la_stream_t stream) {
+    return prefill_packed(q, k, v, o, cu_seqlens, n_seq, T, state_pool, n_pool, init_idx, s_out, H, dk, dv, dt, chunk,
+                          phi, false, nullptr, workspace, ws_bytes, stream);
+}
+
+size_t la_prefill_varlen_decay_workspace_size(int n_seq, int T, int H, int dk, int dv, la_dtype dt) {
+    return la_prefill_varlen_workspace_size_ex(n_seq, T, H, dk, dv, dt, LA_PHI_IDENTITY);
+}
+
+la_status la_prefill_varlen_decay(const void* q, const void* k, const void* v, void* o, const int32_t* cu_seqlens,
+                                  int n_seq, int T, const float* state_pool, int n_pool, const int32_t* init_idx,
+                                  float* s_out, const float* log_decay, int H, int dk, int dv, la_dtype dt, int chunk,
+                                  void* workspace, size_t ws_bytes, la_stream_t stream) {
+    return prefill_packed(q, k, v, o, cu_seqlens, n_seq, T, state_pool, n_pool, init_idx, s_out, H, dk, dv, dt, chunk,
+                          LA_PHI_IDENTITY, true, log_decay, workspace, ws_bytes, stream);
+}
+
+// la_decode_step_ex, and la_decode_step_decay with a log_decay (phi: identity)
+static la_status decode_step(const void* q, const void* k, const void* v, void* o, void* S, int B, int H, int dk,
+                             int dv, la_dtype dt, la_state_dtype sdt, la_phi phi, bool decayed, const float* log_decay,
+                             la_stream_t stream) {
     g_last_error[0] = 0;
     la_status s = check_dims(dk, dv, dt);
     if (s != LA_OK) return s;
@@ -950,24 +1060,36 @@ la_status la_decode_step_ex(const void* q, const void* k, const void* v, void* o
     if (!q || !k || !v || !o || !S) return fail(LA_ERR_INVALID_ARG, "q, k, v, o, S must be non-null");
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(S))
         return fail(LA_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+    if (decayed && !log_decay) return fail(LA_ERR_INVALID_ARG, "log_decay must be non-null");
     DeviceInfo* di;
     if ((s = device_info(&di)) != LA_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (decayed && (s = check_log_decay(log_decay, H, st)) != LA_OK) return s;
     const int grid = (int)U;
     if (dt == LA_FP32) {
-        launch_decode<float, float>(dk, grid, q, k, v, o, S, phi, st);
+        launch_decode<float, float>(dk, grid, q, k, v, o, S, phi, log_decay, H, st);
     } else if (sdt == LA_STATE_FP32) {
-        launch_decode<__nv_bfloat16, float>(dk, grid, q, k, v, o, S, phi, st);
+        launch_decode<__nv_bfloat16, float>(dk, grid, q, k, v, o, S, phi, log_decay, H, st);
     } else if (sdt == LA_STATE_BF16) {
-        launch_decode<__nv_bfloat16, __nv_bfloat16>(dk, grid, q, k, v, o, S, phi, st);
+        launch_decode<__nv_bfloat16, __nv_bfloat16>(dk, grid, q, k, v, o, S, phi, log_decay, H, st);
     } else if (sdt == LA_STATE_FP16) {
-        launch_decode<__nv_bfloat16, __half>(dk, grid, q, k, v, o, S, phi, st);
+        launch_decode<__nv_bfloat16, __half>(dk, grid, q, k, v, o, S, phi, log_decay, H, st);
     } else if (sdt == LA_STATE_FP8_E4M3) {
-        launch_decode<__nv_bfloat16, __nv_fp8_e4m3>(dk, grid, q, k, v, o, S, phi, st);
+        launch_decode<__nv_bfloat16, __nv_fp8_e4m3>(dk, grid, q, k, v, o, S, phi, log_decay, H, st);
     } else {
-        launch_decode<__nv_bfloat16, __nv_fp8_e5m2>(dk, grid, q, k, v, o, S, phi, st);
+        launch_decode<__nv_bfloat16, __nv_fp8_e5m2>(dk, grid, q, k, v, o, S, phi, log_decay, H, st);
     }
     return after_launch("decode_step launch");
+}
+
+la_status la_decode_step_ex(const void* q, const void* k, const void* v, void* o, void* S, int B, int H, int dk,
+                            int dv, la_dtype dt, la_state_dtype sdt, la_phi phi, la_stream_t stream) {
+    return decode_step(q, k, v, o, S, B, H, dk, dv, dt, sdt, phi, false, nullptr, stream);
+}
+
+la_status la_decode_step_decay(const void* q, const void* k, const void* v, void* o, void* S, const float* log_decay,
+                               int B, int H, int dk, int dv, la_dtype dt, la_state_dtype sdt, la_stream_t stream) {
+    return decode_step(q, k, v, o, S, B, H, dk, dv, dt, sdt, LA_PHI_IDENTITY, true, log_decay, stream);
 }
 
 la_status la_decode_step(const void* q, const void* k, const void* v, void* o, float* S, int B, int H, int dk,
@@ -1105,8 +1227,8 @@ extern "C" la_status la_prefill_varlen_noalloc(const void* q, const void* k, con
 // cut into segments as in la_prefill_ex (a state-only pass, then a prefix --
 // in reverse order a suffix -- over the segment sums, then every segment).
 static la_status tc_dense_pass(const void* q, const void* k, const void* v, void* o, const float* init, bool init_t,
-                               float* s_out, bool reverse, long U, int N, int d, DeviceInfo* di, cudaStream_t st,
-                               void* ws, size_t ws_bytes) {
+                               float* s_out, bool reverse, const float* log_decay, int H, long U, int N, int d,
+                               DeviceInfo* di, cudaStream_t st, void* ws, size_t ws_bytes) {
     if (N == 0 && !s_out) return LA_OK;
     const int nvs = tc_slices(d);
     tc::Params p{};
@@ -1123,7 +1245,9 @@ static la_status tc_dense_pass(const void* q, const void* k, const void* v, void
     p.phi = LA_PHI_IDENTITY;
     p.reverse = reverse ? 1 : 0;
     p.init_transposed = init_t ? 1 : 0;
-    const bool wide = use_wide(U, d, di);
+    p.log_decay = log_decay;
+    p.H = H;
+    const bool wide = !log_decay && use_wide(U, d, di);
     int seg_len;
     int P = wide ? 1 : plan_segments(U, N, tc_slices(d), di->sms, &seg_len);
     if (P > 1 && (!ws || ws_bytes < segment_workspace_bytes(U, P, d, d) || !aligned16(ws) ||
@@ -1153,11 +1277,9 @@ static la_status tc_dense_pass(const void* q, const void* k, const void* v, void
         if ((s = launch_tc(std::min(p1.n_items, di->sms), mq, mk, mv, mo, p1, st, "prefill_tc (segment sums) launch")) !=
             LA_OK)
             return s;
-        const long threads = U * (long)(d * d / 4);
-        const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 4L * di->sms);
-        segp::seg_prefix_kernel<<<blocks, segp::NUM_THREADS, 0, st>>>(sums, init, starts, U, P, d * d, reverse ? 1 : 0,
-                                                                     init_t ? 1 : 0, d);
-        if ((s = after_launch("segment prefix launch")) != LA_OK) return s;
+        if ((s = launch_seg_prefix(sums, init, starts, U, P, d, reverse, init_t, log_decay, H, p.seg_len, N, di, st)) !=
+            LA_OK)
+            return s;
         p.n_seg = P;
         p.n_items = (int)(U * P * nvs);
         p.seg_init = starts;
@@ -1187,10 +1309,11 @@ la_status la_prefill_backward(const void* q, const void* k, const void* v, const
                                   stream);
 }
 
-la_status la_prefill_backward_ex(const void* q, const void* k, const void* v, const void* dout, const float* s0,
-                                 const float* ds_n, void* dq, void* dk, void* dv, float* ds0, int B, int H, int N,
-                                 int d_k, int d_v, la_dtype dt, void* workspace, size_t ws_bytes,
-                                 la_stream_t stream) {
+// la_prefill_backward_ex, and la_prefill_decay_backward with a log_decay
+static la_status prefill_backward(const void* q, const void* k, const void* v, const void* dout, const float* s0,
+                                  const float* ds_n, void* dq, void* dk, void* dv, float* ds0, bool decayed,
+                                  const float* log_decay, int B, int H, int N, int d_k, int d_v, la_dtype dt,
+                                  void* workspace, size_t ws_bytes, la_stream_t stream) {
     g_last_error[0] = 0;
     la_status s = check_dims(d_k, d_v, dt);
     if (s != LA_OK) return s;
@@ -1203,9 +1326,11 @@ la_status la_prefill_backward_ex(const void* q, const void* k, const void* v, co
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(dq) || !aligned16(dk) ||
         !aligned16(dv) || !aligned16(s0) || !aligned16(ds_n) || !aligned16(ds0))
         return fail(LA_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+    if (decayed && !log_decay) return fail(LA_ERR_INVALID_ARG, "log_decay must be non-null");
     DeviceInfo* di;
     if ((s = device_info(&di)) != LA_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (decayed && (s = check_log_decay(log_decay, H, st)) != LA_OK) return s;
     // Each gradient is a forward pass over permuted inputs (G_t is the suffix
     // sum dS_N + sum_{t' >= t} q_t'^T do_t'):
     //   dq_t = do_t S_t^T : prefill(dO, V, K) from s0^T
@@ -1213,30 +1338,52 @@ la_status la_prefill_backward_ex(const void* q, const void* k, const void* v, co
     //   dv_t = k_t G_t    : prefill(K, Q, dO) from dS_N, chunks last to first;
     //                       its final state is G_1 = dS_0
     // on the tensor cores for bf16 with d = 128 (unless LA_BACKWARD_SIMT=1),
-    // else on the FFMA path
-    if (use_tensor_cores(d_k, dt) && !env_flag("LA_BACKWARD_SIMT")) {
+    // else on the FFMA path.  With a decay, G_t = q_t^T do_t + lam G_{t+1}: the
+    // same passes, decayed; the reverse ones hold lam G, from dS_N to dS_0
+    // (decay.cuh)
+    if (use_tensor_cores(d_k, dt) && !decayed && !env_flag("LA_BACKWARD_SIMT")) {
         if (N > 0) {
-            if ((s = tc_dense_pass(dout, v, k, dq, s0, true, nullptr, false, U, N, d_k, di, st, workspace, ws_bytes)) !=
+            if ((s = tc_dense_pass(dout, v, k, dq, s0, true, nullptr, false, log_decay, H, U, N, d_k, di, st, workspace, ws_bytes)) !=
                 LA_OK)
                 return s;
-            if ((s = tc_dense_pass(v, dout, q, dk, ds_n, true, nullptr, true, U, N, d_k, di, st, workspace, ws_bytes)) !=
+            if ((s = tc_dense_pass(v, dout, q, dk, ds_n, true, nullptr, true, log_decay, H, U, N, d_k, di, st, workspace, ws_bytes)) !=
                 LA_OK)
                 return s;
         }
         // (the passes run in stream order, so they share the workspace)
-        return tc_dense_pass(k, q, dout, dv, ds_n, false, ds0, true, U, N, d_k, di, st, workspace, ws_bytes);
+        return tc_dense_pass(k, q, dout, dv, ds_n, false, ds0, true, log_decay, H, U, N, d_k, di, st, workspace, ws_bytes);
     }
     if (N == 0 && !ds0) return LA_OK;
     if (N > 0) {
-        if ((s = simt_dense(dout, v, k, dq, s0, true, nullptr, false, LA_PHI_IDENTITY, U, N, d_k, dt, 0, di,
+        if ((s = simt_dense(dout, v, k, dq, s0, true, nullptr, false, LA_PHI_IDENTITY, log_decay, H, U, N, d_k, dt, 0, di,
                             workspace, ws_bytes, st)) != LA_OK)
             return s;
-        if ((s = simt_dense(v, dout, q, dk, ds_n, true, nullptr, true, LA_PHI_IDENTITY, U, N, d_k, dt, 0, di,
+        if ((s = simt_dense(v, dout, q, dk, ds_n, true, nullptr, true, LA_PHI_IDENTITY, log_decay, H, U, N, d_k, dt, 0, di,
                             workspace, ws_bytes, st)) != LA_OK)
             return s;
     }
-    return simt_dense(k, q, dout, dv, ds_n, false, ds0, true, LA_PHI_IDENTITY, U, N, d_k, dt, 0, di, workspace,
+    return simt_dense(k, q, dout, dv, ds_n, false, ds0, true, LA_PHI_IDENTITY, log_decay, H, U, N, d_k, dt, 0, di, workspace,
                       ws_bytes, st);
+}
+
+la_status la_prefill_backward_ex(const void* q, const void* k, const void* v, const void* dout, const float* s0,
+                                 const float* ds_n, void* dq, void* dk, void* dv, float* ds0, int B, int H, int N,
+                                 int d_k, int d_v, la_dtype dt, void* workspace, size_t ws_bytes,
+                                 la_stream_t stream) {
+    return prefill_backward(q, k, v, dout, s0, ds_n, dq, dk, dv, ds0, false, nullptr, B, H, N, d_k, d_v, dt, workspace,
+                            ws_bytes, stream);
+}
+
+size_t la_prefill_decay_backward_workspace_size(int B, int H, int N, int d_k, int d_v, la_dtype dt) {
+    return la_prefill_backward_workspace_size(B, H, N, d_k, d_v, dt);
+}
+
+la_status la_prefill_decay_backward(const void* q, const void* k, const void* v, const void* dout, const float* s0,
+                                    const float* ds_n, const float* log_decay, void* dq, void* dk, void* dv, float* ds0,
+                                    int B, int H, int N, int d_k, int d_v, la_dtype dt, void* workspace,
+                                    size_t ws_bytes, la_stream_t stream) {
+    return prefill_backward(q, k, v, dout, s0, ds_n, dq, dk, dv, ds0, true, log_decay, B, H, N, d_k, d_v, dt, workspace,
+                            ws_bytes, stream);
 }
 
 size_t la_prefill_host_workspace_size(int B, int H, int N, int dk, int dv, la_dtype dt, int group) {
@@ -1338,6 +1485,8 @@ la_status la_prefill_host(const void* q, const void* k, const void* v, void* o, 
     cleanup();
     return LA_OK;
 }
+
+#include "la_norm_rope.cuh"
 
 la_status la_selftest_wait_timeout(int timeout_us, la_stream_t stream) {
     g_last_error[0] = 0;

@@ -17,7 +17,14 @@
 // chunks (and in shared memory for Q S), and the next chunk is prefetched into
 // L2 while this one is loaded.  The chunk length CS (32 or 64) is a template
 // parameter.
+//
+// kDecay: a decay per head (decay.cuh).  The scores take lam^(t - s), the
+// outputs' Q S term lam^(t + 1) per row, the state update K rows times
+// lam^(R - 1 - s) and the old state times lam^R (R rows in the chunk); every
+// factor is fp32 and nothing is rounded below fp32.  Other instances are
+// unchanged by it.
 #pragma once
+#include "decay.cuh"
 #include "phi.cuh"
 #include <cuda_bf16.h>
 
@@ -59,6 +66,8 @@ struct Params {
     const int* seg_off_nl;
     const int* seg_len_dev;
     int n_seq;
+    const float* log_decay; // [heads] log of the decay per head, or null (kDecay instances only)
+    int heads;              // dense: unit u has head u % heads
 };
 
 // Shared-memory layout (floats), rows padded by 4 so that 16-byte vectors
@@ -162,7 +171,7 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, const float* x) {
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-template <typename T, int D, int CS>
+template <typename T, int D, int CS, bool kDecay = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, T* __restrict__ o,
                     const Params p) {
@@ -175,6 +184,7 @@ prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     constexpr int VEC = 16 / sizeof(T);           // elements per 16-byte global load
     constexpr int VPR = D / VEC;                  // 16-byte vectors per row
     extern __shared__ float sf[];
+    __shared__ float lam_n[kDecay ? CS + 1 : 1];  // lam^n, n = 0 .. CS
     float* Qt = sf;
     float* Kt = Qt + D * LQ;
     float* Kn = Kt + D * LQ;
@@ -244,6 +254,15 @@ prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         const int ii = p.init_idx ? p.init_idx[seq] : -1;
         if (p.pool && ii >= 0) init = p.pool + ((long)ii * p.H + h) * D * D;
     }
+    float fh = 1.f, fl = 0.f;  // lam^CS
+    double g = 0.0;
+    if constexpr (kDecay) {
+        const int head = p.mode == 1 ? (int)(blockIdx.x % p.H)
+                                     : (int)((p.n_seg > 0 ? blockIdx.x / p.n_seg : blockIdx.x) % p.heads);
+        g = p.log_decay[head];
+        if (tid <= CS) lam_n[tid] = decay::power(g, tid);
+        decay::power2(g, CS, fh, fl);
+    }
     // the state tile of this thread: rows ty*TM3 + r, columns col_of<TN3, D>(tx, c)
     float accS[TM3][TN3];
 #pragma unroll
@@ -304,6 +323,12 @@ prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
                 Qt[(cc + e) * LQ + t] = qv[e];
                 Kt[(cc + e) * LQ + t] = kv[e];
             }
+            if constexpr (kDecay) {
+                // the state update's weight of this token
+                const float w = t < rows ? lam_n[rev ? t + 1 : rows - 1 - t] : 0.f;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) kv[e] *= w;
+            }
 #pragma unroll
             for (int e = 0; e < VEC; e += 4) {
                 *reinterpret_cast<float4*>(Kn + t * LV + cc + e) = make_float4(kv[e], kv[e + 1], kv[e + 2], kv[e + 3]);
@@ -335,7 +360,11 @@ prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             for (int c = 0; c < TN1; ++c) {
                 float col[TM1];
 #pragma unroll
-                for (int r = 0; r < TM1; ++r) col[r] = (rev ? s0 + c >= t0 + r : s0 + c <= t0 + r) ? acc[r][c] : 0.f;
+                for (int r = 0; r < TM1; ++r) {
+                    const bool keep = rev ? s0 + c >= t0 + r : s0 + c <= t0 + r;
+                    if constexpr (kDecay) col[r] = keep ? acc[r][c] * lam_n[abs(t0 + r - s0 - c)] : 0.f;
+                    else col[r] = keep ? acc[r][c] : 0.f;
+                }
                 st_run<TM1>(At + (s0 + c) * LQ + t0, col);
             }
         }
@@ -349,6 +378,26 @@ prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 #pragma unroll
                 for (int c = 0; c < TN2; ++c) acc[r][c] = 0.f;
             const int smin = rev ? t0 : 0, smax = rev ? rows : min(rows, t0 + TM2);
+            // Q S first with a decay, to scale its rows before the chunk's own
+            // tokens are added
+            if constexpr (kDecay) {
+#pragma unroll 4
+                for (int i = 0; i < D; ++i) {
+                    float a[TM2], b[TN2];
+                    ld_run<TM2>(Qt + i * LQ + t0, a);
+                    ld_cols<TN2, D>(Sm + i * LV, tx, b);
+#pragma unroll
+                    for (int r = 0; r < TM2; ++r)
+#pragma unroll
+                        for (int c = 0; c < TN2; ++c) acc[r][c] = fmaf(a[r], b[c], acc[r][c]);
+                }
+#pragma unroll
+                for (int r = 0; r < TM2; ++r) {
+                    const float w = lam_n[rev ? max(rows - 1 - t0 - r, 0) : t0 + r + 1];
+#pragma unroll
+                    for (int c = 0; c < TN2; ++c) acc[r][c] *= w;
+                }
+            }
 #pragma unroll 2
             for (int s = smin; s < smax; ++s) {
                 float a[TM2], b[TN2];
@@ -359,15 +408,17 @@ prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 #pragma unroll
                     for (int c = 0; c < TN2; ++c) acc[r][c] = fmaf(a[r], b[c], acc[r][c]);
             }
+            if constexpr (!kDecay) {
 #pragma unroll 4
-            for (int i = 0; i < D; ++i) {
-                float a[TM2], b[TN2];
-                ld_run<TM2>(Qt + i * LQ + t0, a);
-                ld_cols<TN2, D>(Sm + i * LV, tx, b);
+                for (int i = 0; i < D; ++i) {
+                    float a[TM2], b[TN2];
+                    ld_run<TM2>(Qt + i * LQ + t0, a);
+                    ld_cols<TN2, D>(Sm + i * LV, tx, b);
 #pragma unroll
-                for (int r = 0; r < TM2; ++r)
+                    for (int r = 0; r < TM2; ++r)
 #pragma unroll
-                    for (int c = 0; c < TN2; ++c) acc[r][c] = fmaf(a[r], b[c], acc[r][c]);
+                        for (int c = 0; c < TN2; ++c) acc[r][c] = fmaf(a[r], b[c], acc[r][c]);
+                }
             }
 #pragma unroll
             for (int r = 0; r < TM2; ++r) {
@@ -382,7 +433,15 @@ prefill_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             }
         }
         __syncthreads();  // every read of Sm for this chunk is done
-        // ---- state: S += K^T V over the chunk's valid rows
+        // ---- state: S += K^T V over the chunk's valid rows (S <- lam^rows S + ... with a decay)
+        if constexpr (kDecay) {
+            if (rows < CS) decay::power2(g, rows, fh, fl);  // the chunk at the sequence's end
+#pragma unroll
+            for (int r = 0; r < TM3; ++r)
+#pragma unroll
+                for (int c = 0; c < TN3; ++c) accS[r][c] = fmaf(accS[r][c], fh, accS[r][c] * fl);
+            if (rows < CS) decay::power2(g, CS, fh, fl);
+        }
 #pragma unroll 2
         for (int s = 0; s < rows; ++s) {
             float a[TM3], b[TN3];

@@ -127,6 +127,7 @@ struct Params {
     const int* seg_off_nl;
     const int* seg_len_dev;
     int n_seq;
+    const float* log_decay; // [H] log of the decay per head (prefill_decay.cuh), or null; dense: head u % H
 };
 
 struct Item {

@@ -8,8 +8,14 @@
 // suffix sums) the state before segment p is S_init plus the sums of segments
 // p+1 .. n_seg-1.  Each thread owns 4 consecutive fp32 elements of one unit's
 // d_k x d_v state and walks the segments in order.
+//
+// kDecay: the sums carry their decay to the segment's end (in reverse order:
+// beyond its start), and the running state is multiplied by lam^len over each
+// segment it passes (decay.cuh): starts[p+1] = lam^len_p starts[p] + sum_p.
 #pragma once
 #include <cuda_runtime.h>
+
+#include "decay.cuh"
 
 namespace lcl {
 namespace segp {
@@ -20,10 +26,14 @@ constexpr int NUM_THREADS = 256;
 // Forward: seg_sums[p] is the sum of segment p, starts[p] = s0 + sum_{p' < p}.
 // Reverse (tokens visited last to first): seg_sums[p] is the sum of segment
 // p + 1, starts[p] = s0 + sum_{p' > p}.  s0_transposed: s0 is given as the
-// transpose of a d x d state (elems = d * d).
+// transpose of a d x d state (elems = d * d).  kDecay: log_decay [H], unit u of
+// head u % H; every segment but the last in memory has seg_len tokens, which
+// has tail_len.
+template <bool kDecay = false>
 __global__ void __launch_bounds__(NUM_THREADS)
 seg_prefix_kernel(const float* __restrict__ seg_sums, const float* __restrict__ s0, float* __restrict__ starts,
-                  long U, int n_seg, int elems, int reverse, int s0_transposed, int d) {
+                  long U, int n_seg, int elems, int reverse, int s0_transposed, int d,
+                  const float* __restrict__ log_decay = nullptr, int H = 1, int seg_len = 0, int tail_len = 0) {
     const int per_unit = elems / 4;
     for (long t = (long)blockIdx.x * blockDim.x + threadIdx.x; t < U * per_unit; t += (long)gridDim.x * blockDim.x) {
         const long u = t / per_unit;
@@ -38,10 +48,17 @@ seg_prefix_kernel(const float* __restrict__ seg_sums, const float* __restrict__ 
         }
         float* dst = starts + (u * n_seg) * (long)elems + e;
         const float* src = seg_sums + (u * (n_seg - 1)) * (long)elems + e;
+        float f = 1.f, f_tail = 1.f;
+        if constexpr (kDecay) {
+            const double g = log_decay[u % H];
+            f = decay::power(g, seg_len);
+            f_tail = decay::power(g, tail_len);
+        }
         if (!reverse) {
             *reinterpret_cast<float4*>(dst) = acc;
             for (int p = 1; p < n_seg; ++p) {
                 const float4 x = *reinterpret_cast<const float4*>(src + (long)(p - 1) * elems);
+                if constexpr (kDecay) { acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f; }
                 acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
                 *reinterpret_cast<float4*>(dst + (long)p * elems) = acc;
             }
@@ -49,6 +66,10 @@ seg_prefix_kernel(const float* __restrict__ seg_sums, const float* __restrict__ 
             *reinterpret_cast<float4*>(dst + (long)(n_seg - 1) * elems) = acc;
             for (int p = n_seg - 2; p >= 0; --p) {
                 const float4 x = *reinterpret_cast<const float4*>(src + (long)p * elems);
+                if constexpr (kDecay) {
+                    const float fp = p == n_seg - 2 ? f_tail : f;
+                    acc.x *= fp; acc.y *= fp; acc.z *= fp; acc.w *= fp;
+                }
                 acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
                 *reinterpret_cast<float4*>(dst + (long)p * elems) = acc;
             }
@@ -61,10 +82,12 @@ seg_prefix_kernel(const float* __restrict__ seg_sums, const float* __restrict__ 
 // before segment g of rank r, head h is pool[init_idx[seq]][h] (or zero) plus
 // the sums of the sequence's segments before g.
 //   seg_sums: [non-last segments][H][elems]   starts: [segments][H][elems]
+template <bool kDecay = false>
 __global__ void __launch_bounds__(NUM_THREADS)
 seg_prefix_varlen_kernel(const float* __restrict__ seg_sums, const float* __restrict__ pool,
                          const int* __restrict__ init_idx, const int* __restrict__ order, const int* __restrict__ seg_off,
-                         const int* __restrict__ seg_off_nl, float* __restrict__ starts, int n_seq, int H, int elems) {
+                         const int* __restrict__ seg_off_nl, float* __restrict__ starts, int n_seq, int H, int elems,
+                         const float* __restrict__ log_decay = nullptr, const int* __restrict__ seg_len = nullptr) {
     const int per_unit = elems / 4;
     const long total = (long)n_seq * H * per_unit;
     for (long t = (long)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += (long)gridDim.x * blockDim.x) {
@@ -77,8 +100,11 @@ seg_prefix_varlen_kernel(const float* __restrict__ seg_sums, const float* __rest
         if (pool && ii >= 0) acc = *reinterpret_cast<const float4*>(pool + ((long)ii * H + h) * elems + e);
         const int s0 = seg_off[r], cnt = seg_off[r + 1] - s0, nl0 = seg_off_nl[r];
         *reinterpret_cast<float4*>(starts + ((long)s0 * H + h) * elems + e) = acc;
+        float f = 1.f;  // every segment that another one follows has *seg_len tokens
+        if constexpr (kDecay) f = decay::power(log_decay[h], *seg_len);
         for (int g = 1; g < cnt; ++g) {
             const float4 x = *reinterpret_cast<const float4*>(seg_sums + ((long)(nl0 + g - 1) * H + h) * elems + e);
+            if constexpr (kDecay) { acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f; }
             acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
             *reinterpret_cast<float4*>(starts + ((long)(s0 + g) * H + h) * elems + e) = acc;
         }
