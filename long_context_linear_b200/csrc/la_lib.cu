@@ -22,6 +22,7 @@
 #include "sm100.cuh"
 #include "prefill_tc.cuh"
 #include "prefill_wide.cuh"
+#include "prefill_decay.cuh"
 #include "prefill_simt.cuh"
 #include "decode.cuh"
 #include "varlen_order.cuh"
@@ -163,6 +164,12 @@ la_status device_info(DeviceInfo** out) {
             (e = set_simt_attrs<__nv_bfloat16, false>()) != cudaSuccess ||
             (e = set_simt_attrs<float, true>()) != cudaSuccess || (e = set_simt_attrs<__nv_bfloat16, true>()) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(prefill_simt)");
+        const void* decay_kernels[2] = {reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64>)};
+        for (const void* kern : decay_kernels)
+            if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tcd::SMEM_BYTES)) !=
+                cudaSuccess)
+                return cuda_fail(e, "cudaFuncSetAttribute(prefill_decay)");
         const unsigned long long id = current_ctx_id();
         if (id != d.ctx) d.h2d = d.d2h = nullptr;  // copy streams of a context that is gone
         d.ctx = id;
@@ -277,7 +284,10 @@ la_status launch_tc(int grid, const CUtensorMap& mq, const CUtensorMap& mk, cons
     const bool general =
         phi || p.reverse || p.state_only || p.init_transposed || (p.mode == 0 && p.n_seg > 1) || p.seg_off;
     auto go = [&](auto kern) { kern<<<grid, tc::NUM_THREADS, tc::SMEM_BYTES, st>>>(mq, mk, mv, mo, p); };
-    if (p.dk == 64) {
+    if (p.log_decay) {
+        if (p.dk == 64) tcd::prefill_decay_kernel<64><<<grid, tcd::NUM_THREADS, tcd::SMEM_BYTES, st>>>(mq, mk, mv, mo, p);
+        else tcd::prefill_decay_kernel<128><<<grid, tcd::NUM_THREADS, tcd::SMEM_BYTES, st>>>(mq, mk, mv, mo, p);
+    } else if (p.dk == 64) {
         if (phi) go(tc::prefill_tc_kernel<true, true, 64>);
         else if (general) go(tc::prefill_tc_kernel<true, false, 64>);
         else go(tc::prefill_tc_kernel<false, false, 64>);
@@ -656,7 +666,7 @@ static la_status prefill_dense(const void* q, const void* k, const void* v, void
     if (N > 0 && (!q || !k || !v || !o)) return fail(LA_ERR_INVALID_ARG, "q, k, v, o must be non-null");
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(s0) || !aligned16(s_out))
         return fail(LA_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
-    const bool tcpath = tensor_core_path(dk, dt, chunk) && !decayed;
+    const bool tcpath = tensor_core_path(dk, dt, chunk);
     if ((s = check_chunk(chunk, tcpath)) != LA_OK) return s;
     if (decayed && !log_decay) return fail(LA_ERR_INVALID_ARG, "log_decay must be non-null");
     DeviceInfo* di;
@@ -854,7 +864,7 @@ static la_status prefill_packed(const void* q, const void* k, const void* v, voi
         (reinterpret_cast<uintptr_t>(init_idx) & 3u))
         return fail(LA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned, index arrays 4-byte aligned");
     if ((long)T * H > (1L << 40) || (long)n_seq * H > (1L << 30)) return fail(LA_ERR_INVALID_ARG, "problem too large");
-    const bool tcpath = tensor_core_path(dk, dt, chunk) && !decayed;
+    const bool tcpath = tensor_core_path(dk, dt, chunk);
     if ((s = check_chunk(chunk, tcpath)) != LA_OK) return s;
     const size_t need = varlen_order_bytes(n_seq);
     if (tcpath && (ws_bytes < need || !workspace || !aligned16(workspace)))
@@ -1341,7 +1351,7 @@ static la_status prefill_backward(const void* q, const void* k, const void* v, c
     // else on the FFMA path.  With a decay, G_t = q_t^T do_t + lam G_{t+1}: the
     // same passes, decayed; the reverse ones hold lam G, from dS_N to dS_0
     // (decay.cuh)
-    if (use_tensor_cores(d_k, dt) && !decayed && !env_flag("LA_BACKWARD_SIMT")) {
+    if (use_tensor_cores(d_k, dt) && !env_flag("LA_BACKWARD_SIMT")) {
         if (N > 0) {
             if ((s = tc_dense_pass(dout, v, k, dq, s0, true, nullptr, false, log_decay, H, U, N, d_k, di, st, workspace, ws_bytes)) !=
                 LA_OK)
