@@ -164,8 +164,10 @@ la_status device_info(DeviceInfo** out) {
             (e = set_simt_attrs<__nv_bfloat16, false>()) != cudaSuccess ||
             (e = set_simt_attrs<float, true>()) != cudaSuccess || (e = set_simt_attrs<__nv_bfloat16, true>()) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(prefill_simt)");
-        const void* decay_kernels[2] = {reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128>),
-                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64>)};
+        const void* decay_kernels[4] = {reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, false>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, true>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, false>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, true>)};
         for (const void* kern : decay_kernels)
             if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tcd::SMEM_BYTES)) !=
                 cudaSuccess)
@@ -285,8 +287,9 @@ la_status launch_tc(int grid, const CUtensorMap& mq, const CUtensorMap& mk, cons
         phi || p.reverse || p.state_only || p.init_transposed || (p.mode == 0 && p.n_seg > 1) || p.seg_off;
     auto go = [&](auto kern) { kern<<<grid, tc::NUM_THREADS, tc::SMEM_BYTES, st>>>(mq, mk, mv, mo, p); };
     if (p.log_decay) {
-        if (p.dk == 64) tcd::prefill_decay_kernel<64><<<grid, tcd::NUM_THREADS, tcd::SMEM_BYTES, st>>>(mq, mk, mv, mo, p);
-        else tcd::prefill_decay_kernel<128><<<grid, tcd::NUM_THREADS, tcd::SMEM_BYTES, st>>>(mq, mk, mv, mo, p);
+        auto god = [&](auto kern) { kern<<<grid, tcd::NUM_THREADS, tcd::SMEM_BYTES, st>>>(mq, mk, mv, mo, p); };
+        if (p.dk == 64) p.reverse ? god(tcd::prefill_decay_kernel<64, true>) : god(tcd::prefill_decay_kernel<64, false>);
+        else p.reverse ? god(tcd::prefill_decay_kernel<128, true>) : god(tcd::prefill_decay_kernel<128, false>);
     } else if (p.dk == 64) {
         if (phi) go(tc::prefill_tc_kernel<true, true, 64>);
         else if (general) go(tc::prefill_tc_kernel<true, false, 64>);

@@ -5,7 +5,7 @@
 // exp(log_decay[head]) (decay.cuh):
 //
 //   [P | Oqs] = Q_c [K_c ; bf16(S)^T]^T     one N = 192 product, fp32 in TMEM
-//   P[l][m]  <- lam^(l-m) P[l][m], m <= l    fp32 factor, then bf16, into a TMEM buffer of its own
+//   P[l][m]  <- lam^(l-m) P[l][m], m <= l    fp32 factor, then bf16, in place
 //   Opv       = P V_c                        A = P from TMEM
 //   O[l]      = Opv[l] + lam^(l+1) Oqs[l]    joined in fp32 on the way out
 //   dS        = K_c^T [V1 | V2 | V3]         one N = 192 product; V1 + V2 + V3 = lam^(R-1-m) V
@@ -30,12 +30,12 @@
 // and S^T form one run of rows (in slot 1 S^T comes first and the accumulator's
 // columns swap); V 2 x 16 KB; the three V terms 48 KB.  O is staged in its
 // chunk's V slot, whose last readers are the products that made it.
-// TMEM (512 columns): [P | Oqs] 192, bf16 P 64, Opv 64, dS 192.
+// TMEM (of 512 columns): [P | Oqs] 192, Opv 64, dS 192.
 //
 // Warp roles (16 warps):
 //   w0 lane 0  : TMA producer for Q and K
 //   w15 lane 0 : TMA producer for V
-//   w1 lane 0  : MMA thread A: [P | Oqs] of chunk c+1, then P V of chunk c
+//   w1 lane 0  : MMA thread A: [P | Oqs], then P V
 //   w14 lane 0 : MMA thread B: dS
 //   w2..w5     : V terms of a chunk, then its masked and decayed P
 //   w6..w9     : state warps (publish bf16(S)^T, absorb dS)
@@ -73,9 +73,9 @@ constexpr int BAR_V_EMPTY = BAR_V_FULL + SLOTS;    // [2] output warps (O stored
 constexpr int BAR_VT_FULL = BAR_V_EMPTY + SLOTS;   // [2] by chunk parity: P warps (terms written) -> B
 constexpr int BAR_VT_EMPTY = BAR_VT_FULL + SLOTS;  // B (dS) -> P warps
 constexpr int BAR_F_FULL = BAR_VT_EMPTY + 1;       // A ([P|Oqs]) -> P warps, output warps
-constexpr int BAR_F_FREE = BAR_F_FULL + 1;         // P warps + output warps (read) -> A
+constexpr int BAR_F_FREE = BAR_F_FULL + 1;         // output warps (Oqs read) -> A
 constexpr int BAR_P_READY = BAR_F_FREE + 1;        // P warps (bf16 P written) -> A
-constexpr int BAR_O_FULL = BAR_P_READY + 1;        // A (P V) -> output warps, P warps
+constexpr int BAR_O_FULL = BAR_P_READY + 1;        // A (P V) -> output warps, A
 constexpr int BAR_O_EMPTY = BAR_O_FULL + 1;        // output warps (Opv read) -> A
 constexpr int BAR_DS_FULL = BAR_O_EMPTY + 1;       // B -> state warps
 constexpr int BAR_DS_EMPTY = BAR_DS_FULL + 1;      // state warps -> B
@@ -88,7 +88,8 @@ constexpr int BAR_COUNT = BAR_DRAIN_B + 1;
 constexpr int BAR_BYTES = 256;
 static_assert((BAR_COUNT + 2) * 8 <= BAR_BYTES, "barrier area too small");
 constexpr int OFF_TAB = OFF_BAR + BAR_BYTES;       // lam^n, n = 0 .. C, by item parity
-constexpr int TAB = C + 4;
+constexpr int TAB_PAD = 32;                        // entries in front of lam^0
+constexpr int TAB = TAB_PAD + C + 4;
 constexpr int SMEM_BYTES = OFF_TAB + 2 * TAB * 4 + 1024;
 static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
 constexpr int NUM_THREADS = 512;
@@ -97,15 +98,16 @@ constexpr int WARP_MMA_B = 14;
 constexpr int WARP_LOAD_V = 15;
 
 constexpr uint32_t TM_F = 0;       // [P | Oqs]; [Oqs | P] in slot 1
-constexpr uint32_t TM_PB = 192;    // bf16 P
-constexpr uint32_t TM_OPV = 256;
-constexpr uint32_t TM_DS = 320;    // three terms of 64 columns
+constexpr uint32_t TM_OPV = 192;
+constexpr uint32_t TM_DS = 256;    // three terms of 64 columns
 constexpr uint32_t TMEM_COLS = 512;
 
 // Shared-memory offsets of K slot s and of S^T inside a panel.
 __device__ __forceinline__ constexpr int k_off(int s) { return s ? PANEL + ST_BYTES : 0; }
 
-// The weighted V terms of a chunk, by the 128 threads t of the P warps: 16-byte
+// The weighted V terms of a chunk (fp32 cut into three runs of 8 bits: each
+// term is the upper half of what is left, so no conversion is needed and the
+// three hold all 24 bits), by the 128 threads t of the P warps: 16-byte
 // vectors of 8 values; a vector's place in the (swizzled) tile is the same in
 // all four tiles, its row is place / 8.  Rows from `rows` on become zero; with
 // `clear` (packed batch: they hold another sequence's tokens, or anything) they
@@ -113,7 +115,7 @@ __device__ __forceinline__ constexpr int k_off(int s) { return s ? PANEL + ST_BY
 template <int NP>
 __device__ __forceinline__ void v_terms(uint32_t v, uint32_t vt, uint32_t k, const float* tab, int t, int rows, bool rev,
                                         bool clear) {
-#pragma unroll 2
+#pragma unroll 1
     for (int j = 0; j < PANEL / 16 / 128; ++j) {
         const int e = t + j * 128, row = e >> 3;
         const uint32_t off = static_cast<uint32_t>(e) * 16u;
@@ -130,17 +132,19 @@ __device__ __forceinline__ void v_terms(uint32_t v, uint32_t vt, uint32_t k, con
         const float w = tab[rev ? row + 1 : rows - 1 - row];
         const uint4 r = ld_shared_v4(v + off);
         const uint32_t in[4] = {r.x, r.y, r.z, r.w};
+        const uint64_t w2 = f32x2(w, w), minus = f32x2(-1.f, -1.f);
         uint32_t out[TERMS][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float lo = __uint_as_float(in[i] << 16) * w, hi = __uint_as_float(in[i] & 0xffff0000u) * w;
+            uint64_t x = mul2(f32x2(in[i] << 16, in[i] & 0xffff0000u), w2);
 #pragma unroll
             for (int n = 0; n < TERMS; ++n) {
-                const uint32_t p = pack_bf16x2(lo, hi);
-                out[n][i] = p;
-                // the remainder, exact: the difference of nearby floats
-                lo -= __uint_as_float(p << 16);
-                hi -= __uint_as_float(p & 0xffff0000u);
+                float lo, hi;
+                f32x2_split(x, lo, hi);
+                const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
+                out[n][i] = __byte_perm(a, b, 0x7632);
+                // the remainder: the bits cut off, exact
+                if (n + 1 < TERMS) x = fma2(f32x2(a & 0xffff0000u, b & 0xffff0000u), minus, x);
             }
         }
 #pragma unroll
@@ -148,7 +152,23 @@ __device__ __forceinline__ void v_terms(uint32_t v, uint32_t vt, uint32_t k, con
     }
 }
 
+// Out of line, one copy for all roles: they run once per item, and the
+// kernel's instruction footprint is what its loops wait for (all roles of all
+// SMs run at once; 112 KB with these inlined, P and the V terms unrolled and
+// both orders in one instance took 10,000 cycles per chunk).
 template <int KD>
+__device__ __noinline__ tc::Item item(const tc::Params& p, int idx) {
+    return tc::decode_item<true, KD>(p, idx);
+}
+// lam^n as two fp32 values, for the head of `it`
+__device__ __noinline__ float2 item_power(const tc::Params& p, int c1, int c2, int n) {
+    float2 f;
+    decay::power2(p.log_decay[p.mode == 0 ? c2 % p.H : c1], n, f.x, f.y);
+    return f;
+}
+
+// kRev: chunks visited last to first (the backward's reverse passes).
+template <int KD, bool kRev>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
@@ -184,7 +204,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const int G = gridDim.x;
     const int cta = blockIdx.x;
     const bool state_only = p.state_only;
-    const bool rev = p.reverse;
+    constexpr bool rev = kRev;
     constexpr int NP = KD / 64;  // 64-column panels per Q / K tile
 
     if (threadIdx.x == 0) {
@@ -199,7 +219,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         mbar_init(vt_empty, 1);
         mbar_init(f_full, 1);
-        mbar_init(f_free, 8);
+        mbar_init(f_free, 4);
         mbar_init(p_ready, 4);
         mbar_init(o_full, 1);
         mbar_init(o_empty, 4);
@@ -236,7 +256,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (int r = 0; !stop; ++r) {
                 const int idx = tc::item_index(r, cta, G);
                 if (idx >= p.n_items) break;
-                const tc::Item it = tc::decode_item<true, KD>(p, idx);
+                const tc::Item it = item<KD>(p, idx);
                 const int nc = (it.len + C - 1) / C;
                 for (int c = 0; c < nc; ++c) {
                     const int t = it.t0 + tc::chunk_row(rev, c, nc);
@@ -275,7 +295,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (int r = 0; !stop; ++r) {
                 const int idx = tc::item_index(r, cta, G);
                 if (idx >= p.n_items) break;
-                const tc::Item it = tc::decode_item<true, KD>(p, idx);
+                const tc::Item it = item<KD>(p, idx);
                 const int nc = (it.len + C - 1) / C;
                 for (int c = 0; c < nc; ++c, ++g) {
                     const int t = it.t0 + tc::chunk_row(rev, c, nc);
@@ -298,39 +318,38 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (int r = 0;; ++r) {
                 const int idx = tc::item_index(r, cta, G);
                 if (idx >= p.n_items) break;
-                total += (tc::decode_item<true, KD>(p, idx).len + C - 1) / C;
+                total += (item<KD>(p, idx).len + C - 1) / C;
             }
-            for (int x = 0; x <= total && total > 0; ++x) {
-                // [P | Oqs] of chunk x, once Q, K and S^T are there and chunk x-1's have been read
-                if (x < total) {
-                    const int s = x % SLOTS;
-                    if (!mbar_wait(s_full, x & 1, abort, p.status)) break;
-                    if (!mbar_wait(&q_full[s], (x / SLOTS) & 1, abort, p.status)) break;
-                    if (!mbar_wait(&k_full[s], (x / SLOTS) & 1, abort, p.status)) break;
-                    if (x > 0 && !mbar_wait(f_free, (x - 1) & 1, abort, p.status)) break;
-                    tc_fence_after();
-                    const uint64_t da = tc::kmaj_desc(sq + s * TILE_Q, 0, PANEL);
-                    const uint64_t db = tc::kmaj_desc(sk + (s ? PANEL : 0), 0, KPAN);
+            for (int g = 0; g < total; ++g) {
+                // [P | Oqs], once Q, K and S^T are there, the output warps have read
+                // Oqs of the chunk before and its P V (of another shape, so not
+                // ordered before this product by itself) has read P
+                const int s = g % SLOTS;
+                if (!mbar_wait(s_full, g & 1, abort, p.status)) break;
+                if (!mbar_wait(&q_full[s], (g / SLOTS) & 1, abort, p.status)) break;
+                if (!mbar_wait(&k_full[s], (g / SLOTS) & 1, abort, p.status)) break;
+                if (g > 0 && !mbar_wait(f_free, (g - 1) & 1, abort, p.status)) break;
+                if (g > 0 && !mbar_wait(o_full, (g - 1) & 1, abort, p.status)) break;
+                tc_fence_after();
+                const uint64_t da = tc::kmaj_desc(sq + s * TILE_Q, 0, PANEL);
+                const uint64_t db = tc::kmaj_desc(sk + (s ? PANEL : 0), 0, KPAN);
 #pragma unroll
-                    for (int kk = 0; kk < KD / 16; ++kk)
-                        mma_ss(tbase + TM_F, da + tc::kmaj_step(kk, PANEL), db + tc::kmaj_step(kk, KPAN), id_f, kk > 0);
-                    mma_commit(f_full);
-                    mma_commit(&q_empty[s]);
-                    mma_commit(&k_empty[s]);
-                    mma_commit(st_free);
-                }
-                // P V of chunk x-1
-                if (x > 0) {
-                    const int g = x - 1, s = g % SLOTS;
-                    if (!mbar_wait(p_ready, g & 1, abort, p.status)) break;
-                    if (g > 0 && !mbar_wait(o_empty, (g - 1) & 1, abort, p.status)) break;
-                    tc_fence_after();
-                    const uint64_t dv = tc::mnmaj_desc(sv + s * PANEL, 0, PANEL);
+                for (int kk = 0; kk < KD / 16; ++kk)
+                    mma_ss(tbase + TM_F, da + tc::kmaj_step(kk, PANEL), db + tc::kmaj_step(kk, KPAN), id_f, kk > 0);
+                mma_commit(f_full);
+                mma_commit(&q_empty[s]);
+                mma_commit(&k_empty[s]);
+                mma_commit(st_free);
+                // P V
+                if (!mbar_wait(p_ready, g & 1, abort, p.status)) break;
+                if (g > 0 && !mbar_wait(o_empty, (g - 1) & 1, abort, p.status)) break;
+                tc_fence_after();
+                const uint32_t tp = tbase + TM_F + (s ? DVS : 0);
+                const uint64_t dv = tc::mnmaj_desc(sv + s * PANEL, 0, PANEL);
 #pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk)
-                        mma_ts(tbase + TM_OPV, tbase + TM_PB + kk * 8, dv + tc::mnmaj_step(kk), id_pv, kk > 0);
-                    mma_commit(o_full);
-                }
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_ts(tbase + TM_OPV, tp + kk * 8, dv + tc::mnmaj_step(kk), id_pv, kk > 0);
+                mma_commit(o_full);
             }
             // every MMA issued by this thread must be finished before TMEM is freed
             mma_commit(drain_a);
@@ -348,7 +367,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (int r = 0; !stop; ++r) {
                 const int idx = tc::item_index(r, cta, G);
                 if (idx >= p.n_items) break;
-                const int len = tc::decode_item<true, KD>(p, idx).len;
+                const int len = item<KD>(p, idx).len;
                 for (int c0 = 0; c0 < len; c0 += C, ++g) {
                     const int s = g % SLOTS;
                     if (!mbar_wait(&k_full[s], (g / SLOTS) & 1, abort, p.status)) { stop = true; break; }
@@ -380,13 +399,12 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         for (int r = 0; !stop; ++r) {
             const int idx = tc::item_index(r, cta, G);
             if (idx >= p.n_items) break;
-            const tc::Item it = tc::decode_item<true, KD>(p, idx);
-            const double ld = p.log_decay[p.mode == 0 ? it.c2 % p.H : it.c1];
+            const tc::Item it = item<KD>(p, idx);
             // the item's table; the other one may still be read by a warp at the
             // item before, and nobody is two items behind (each waits here)
-            float* tab = reinterpret_cast<float*>(sm + OFF_TAB) + (r & 1) * TAB;
-            tab[t] = decay::power(ld, t);
-            if (t == 0) tab[C] = decay::power(ld, C);
+            float* tab = reinterpret_cast<float*>(sm + OFF_TAB) + (r & 1) * TAB + TAB_PAD;
+            tab[t + 1] = item_power(p, it.c1, it.c2, t + 1).x;
+            if (t == 0) tab[0] = 1.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(tab_full);
             if (!tc::warp_wait(tab_full, r & 1, abort, p.status)) break;
@@ -414,47 +432,43 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 if (!tc::warp_wait(f_full, g & 1, abort, p.status)) { stop = true; break; }
                 tc_fence_after();
                 const uint32_t tp = tlane + TM_F + (s ? DVS : 0);
-                uint32_t pk[64];
-#pragma unroll
+#pragma unroll 1
                 for (int pc = 0; pc < 4; ++pc) {
+                    uint32_t pk[16];
                     if (rev ? pc < q4 : pc > q4) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[16 * pc + i] = 0u;
-                        continue;
-                    }
-                    uint32_t v[32];
-                    tmem_ld32(tp + 32 * pc, v);
-                    tmem_wait_ld();
-                    if (pc == q4) {
-                        const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float a = tab[abs(lane - 2 * i)], b = tab[abs(lane - 2 * i - 1)];
-                            pk[16 * pc + i] = pack_bf16x2((keep & (1u << (2 * i))) ? __uint_as_float(v[2 * i]) * a : 0.f,
-                                                          (keep & (2u << (2 * i))) ? __uint_as_float(v[2 * i + 1]) * b : 0.f);
-                        }
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
                     } else {
-                        const float rf = tab[rev ? 32 * pc - row : row - 32 * pc - 31];
+                        uint32_t v[32];
+                        tmem_ld32(tp + 32 * pc, v);
+                        tmem_wait_ld();
+                        if (pc == q4) {
+                            // (the entries in front of lam^0 are read for masked places only)
+                            const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+                            const float* f = rev ? tab - lane : tab + lane;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float a = tab[rev ? 2 * i : 31 - 2 * i], b = tab[rev ? 2 * i + 1 : 30 - 2 * i];
-                            pk[16 * pc + i] =
-                                pack_bf16x2(__uint_as_float(v[2 * i]) * (rf * a), __uint_as_float(v[2 * i + 1]) * (rf * b));
+                            for (int i = 0; i < 16; ++i) {
+                                const float a = f[rev ? 2 * i : -2 * i], b = f[rev ? 2 * i + 1 : -2 * i - 1];
+                                pk[i] = pack_bf16x2((keep & (1u << (2 * i))) ? __uint_as_float(v[2 * i]) * a : 0.f,
+                                                    (keep & (2u << (2 * i))) ? __uint_as_float(v[2 * i + 1]) * b : 0.f);
+                            }
+                        } else {
+                            const float rf = tab[rev ? 32 * pc - row : row - 32 * pc - 31];
+                            const uint64_t rf2 = f32x2(rf, rf);
+                            const float4* col = reinterpret_cast<const float4*>(tab);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                // lam^(4 i) .. lam^(4 i + 3) for columns 4 i .. in reverse order, 31 - 4 i .. in order
+                                const float4 f = col[rev ? i : 7 - i];
+                                const uint64_t f0 = rev ? f32x2(f.x, f.y) : f32x2(f.w, f.z);
+                                const uint64_t f1 = rev ? f32x2(f.z, f.w) : f32x2(f.y, f.x);
+                                pk[2 * i] = pack_bf16x2(mul2(f32x2(v[4 * i], v[4 * i + 1]), mul2(rf2, f0)));
+                                pk[2 * i + 1] = pack_bf16x2(mul2(f32x2(v[4 * i + 2], v[4 * i + 3]), mul2(rf2, f1)));
+                            }
                         }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(f_free);
-                // P V of the chunk before has read the old bf16 P
-                if (g > 0 && !tc::warp_wait(o_full, (g - 1) & 1, abort, p.status)) { stop = true; break; }
-                tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t x[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = pk[32 * h + i];
-                    tmem_st32(tlane + TM_PB + 32 * h, x);
+                    // over fp32 pieces that have been read
+                    tmem_st16(tp + 16 * pc, pk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -470,32 +484,31 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const uint32_t tds = tbase + (static_cast<uint32_t>(q4 * 32) << 16) + TM_DS;
         // bf16(S[i][j]) goes to row j of S^T, key dim i
         const uint32_t colchunk = static_cast<uint32_t>((i & 63) >> 3);
-        uint8_t* st_base = sm + OFF_K + (i >> 6) * KPAN + PANEL + (i & 7) * 2;
+        const uint32_t st_base = smem_u32(sm + OFF_K + (i >> 6) * KPAN + PANEL) + (i & 7) * 2;
         int g = 0;
         bool stop = false;
         for (int r = 0; !stop; ++r) {
             const int idx = tc::item_index(r, cta, G);
             if (idx >= p.n_items) break;
-            const tc::Item it = tc::decode_item<true, KD>(p, idx);
-            const double ld = p.log_decay[p.mode == 0 ? it.c2 % p.H : it.c1];
-            float S[DVS];
+            const tc::Item it = item<KD>(p, idx);
+            uint64_t S[DVS / 2];  // pairs of value columns
             if (it.init && p.init_transposed && own) {
                 const float* src = it.init + (long)DVS * it.vs * KD + i;
 #pragma unroll
-                for (int j = 0; j < DVS; ++j) S[j] = src[j * KD];
+                for (int j = 0; j < DVS; j += 2) S[j / 2] = f32x2(src[j * KD], src[(j + 1) * KD]);
             } else if (it.init && own) {
                 const float4* src = reinterpret_cast<const float4*>(it.init + (long)i * p.dv + DVS * it.vs);
 #pragma unroll
                 for (int j = 0; j < DVS / 4; ++j) {
                     const float4 x = src[j];
-                    S[4 * j] = x.x; S[4 * j + 1] = x.y; S[4 * j + 2] = x.z; S[4 * j + 3] = x.w;
+                    S[2 * j] = f32x2(x.x, x.y);
+                    S[2 * j + 1] = f32x2(x.z, x.w);
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < DVS; ++j) S[j] = 0.f;
+                for (int j = 0; j < DVS / 2; ++j) S[j] = 0ull;
             }
-            float fh_c, fl_c;  // lam^C
-            decay::power2(ld, C, fh_c, fl_c);
+            const float2 lam_c = item_power(p, it.c1, it.c2, C);
             const int nc = (it.len + C - 1) / C;
             for (int c = 0; c < nc; ++c, ++g) {
                 const int rows = min(C, it.len - tc::chunk_row(rev, c, nc));
@@ -504,16 +517,19 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     if (g > 0 && !tc::warp_wait(st_free, (g - 1) & 1, abort, p.status)) { stop = true; break; }
                     if (own) {
 #pragma unroll
-                        for (int j = 0; j < DVS; ++j)
-                            reinterpret_cast<__nv_bfloat16*>(
-                                st_base + j * 128 + ((colchunk ^ static_cast<uint32_t>(j & 7)) << 4))[0] = __float2bfloat16_rn(S[j]);
+                        for (int j = 0; j < DVS; j += 2) {
+                            const uint32_t x = pack_bf16x2(S[j / 2]);
+                            st_shared_b16(st_base + j * 128 + ((colchunk ^ (j & 7)) << 4), static_cast<unsigned short>(x));
+                            st_shared_b16(st_base + (j + 1) * 128 + ((colchunk ^ ((j + 1) & 7)) << 4),
+                                          static_cast<unsigned short>(x >> 16));
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_full);
                 }
-                float fh = fh_c, fl = fl_c;
-                if (rows < C) decay::power2(ld, rows, fh, fl);
+                float2 lam = lam_c;  // lam^rows
+                if (rows < C) lam = item_power(p, it.c1, it.c2, rows);
                 if (!tc::warp_wait(ds_full, g & 1, abort, p.status)) { stop = true; break; }
                 tc_fence_after();
 #pragma unroll
@@ -523,11 +539,12 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     tmem_ld16(tds + DVS + 16 * h, b);
                     tmem_ld16(tds + 2 * DVS + 16 * h, d);
                     tmem_wait_ld();
+                    const uint64_t fh = f32x2(lam.x, lam.x), fl = f32x2(lam.y, lam.y);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float& x = S[16 * h + j];
-                        const float low = __uint_as_float(b[j]) + __uint_as_float(d[j]);
-                        x = fmaf(x, fh, __uint_as_float(a[j])) + fmaf(x, fl, low);
+                    for (int j = 0; j < 16; j += 2) {
+                        uint64_t& x = S[8 * h + j / 2];
+                        const uint64_t low = add2(f32x2(b[j], b[j + 1]), f32x2(d[j], d[j + 1]));
+                        x = add2(fma2(x, fh, f32x2(a[j], a[j + 1])), fma2(x, fl, low));
                     }
                 }
                 tc_fence_before();
@@ -538,8 +555,12 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (p.s_out && it.write_state && own) {
                 float4* dst = reinterpret_cast<float4*>(p.s_out + (it.state * KD + i) * p.dv + DVS * it.vs);
 #pragma unroll
-                for (int j = 0; j < DVS / 4; ++j)
-                    dst[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+                for (int j = 0; j < DVS / 4; ++j) {
+                    float4 x;
+                    f32x2_split(S[2 * j], x.x, x.y);
+                    f32x2_split(S[2 * j + 1], x.z, x.w);
+                    dst[j] = x;
+                }
             }
         }
     } else if (warp < 14) {
@@ -554,7 +575,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             for (int r = 0; !stop; ++r) {
                 const int idx = tc::item_index(r, cta, G);
                 if (idx >= p.n_items) break;
-                const tc::Item it = tc::decode_item<true, KD>(p, idx);
+                const tc::Item it = item<KD>(p, idx);
                 const float g2 = p.log_decay[p.mode == 0 ? it.c2 % p.H : it.c1] * 1.4426950408889634f;
                 const int nc = (it.len + C - 1) / C;
                 for (int c = 0; c < nc; ++c, ++g) {
@@ -567,18 +588,10 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     // --- Oqs, read out early: the next chunk's product overwrites it
                     if (!tc::warp_wait(f_full, g & 1, abort, p.status)) { stop = true; break; }
                     tc_fence_after();
-                    uint32_t qs[64];
-                    {
-                        const uint32_t ta = tlane + TM_F + (s ? 0 : C);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t x[32];
-                            tmem_ld32(ta + 32 * h, x);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) qs[32 * h + i] = x[i];
-                        }
-                        tmem_wait_ld();
-                    }
+                    uint32_t q0[32], q1[32];
+                    tmem_ld32(tlane + TM_F + (s ? 0 : C), q0);
+                    tmem_ld32(tlane + TM_F + (s ? 0 : C) + 32, q1);
+                    tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -593,17 +606,17 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     if (!tc::warp_wait(o_full, g & 1, abort, p.status)) { stop = true; break; }
                     tc_fence_after();
                     uint32_t hp[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    const uint64_t f2 = f32x2(fac, fac);
+                    auto join = [&](int h, const uint32_t (&qs)[32]) {
                         uint32_t x[32];
                         tmem_ld32(tlane + TM_OPV + 32 * h, x);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            hp[16 * h + i] = pack_bf16x2(
-                                fmaf(__uint_as_float(qs[32 * h + 2 * i]), fac, __uint_as_float(x[2 * i])),
-                                fmaf(__uint_as_float(qs[32 * h + 2 * i + 1]), fac, __uint_as_float(x[2 * i + 1])));
-                    }
+                            hp[16 * h + i] = pack_bf16x2(fma2(f32x2(qs[2 * i], qs[2 * i + 1]), f2, f32x2(x[2 * i], x[2 * i + 1])));
+                    };
+                    join(0, q0);
+                    join(1, q1);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(o_empty);
