@@ -39,9 +39,9 @@
 //   w1 lane 0  : MMA thread A: Q K^T
 //   w14 lane 0 : MMA thread B: dS
 //   w15 lane 0 : MMA thread C: P V, Q S
-//   w2..w5     : P warps (masked and decayed P, then the V terms of rows 0 .. 63)
-//   w6..w9     : state warps (publish bf16(S), absorb dS)
-//   w10..w13   : output warps (V terms of rows 64 .. 127, then O)
+//   w2..w5     : P warps (V terms of rows 0 .. 63, then masked and decayed P)
+//   w6..w9     : state warps (V terms of rows 64 .. 127, publish bf16(S), absorb dS)
+//   w10..w13   : output warps
 // Q K^T, P and P V need no state and run ahead; the chain from chunk to chunk
 // is terms -> dS -> S -> Q S.  Every wait is bounded (mbar_wait); a timeout
 // stops the CTA cleanly.
@@ -69,11 +69,11 @@ constexpr int BAR_Q_FULL = 0;                      // [2] TMA -> A, C
 constexpr int BAR_Q_EMPTY = BAR_Q_FULL + SLOTS;    // [2] A (Q K^T) + C (Q S) -> TMA
 constexpr int BAR_K_FULL = BAR_Q_EMPTY + SLOTS;    // [2] TMA -> A, B, P warps (ragged tail)
 constexpr int BAR_K_EMPTY = BAR_K_FULL + SLOTS;    // [2] A (Q K^T) + B (dS) -> TMA
-constexpr int BAR_V_FULL = BAR_K_EMPTY + SLOTS;    // [2] TMA -> P warps, output warps
-constexpr int BAR_V_READ = BAR_V_FULL + SLOTS;     // [2] P warps, output warps (terms formed) -> output warps: V may be overwritten
+constexpr int BAR_V_FULL = BAR_K_EMPTY + SLOTS;    // [2] TMA -> P warps, state warps
+constexpr int BAR_V_READ = BAR_V_FULL + SLOTS;     // [2] P warps, state warps (terms formed) -> output warps: V may be overwritten
 constexpr int BAR_V_EMPTY = BAR_V_READ + SLOTS;    // [2] output warps (O stored from the slot) -> TMA
-constexpr int BAR_VT_FULL = BAR_V_EMPTY + SLOTS;   // [2] by half of the rows: P warps, output warps -> B
-constexpr int BAR_VT_EMPTY = BAR_VT_FULL + 2;      // [2] by half: B (dS) -> P warps, output warps
+constexpr int BAR_VT_FULL = BAR_V_EMPTY + SLOTS;   // [2] by half of the rows: P warps, state warps -> B
+constexpr int BAR_VT_EMPTY = BAR_VT_FULL + 2;      // [2] by half: B (dS) -> P warps, state warps
 constexpr int BAR_P_FULL = BAR_VT_EMPTY + 2;       // [2] A (Q K^T) -> P warps
 constexpr int BAR_P_READY = BAR_P_FULL + 2;        // [2] P warps (bf16 P written, V landed) -> C
 constexpr int BAR_O_FULL = BAR_P_READY + 2;        // C (P V, Q S) -> output warps, state warps
@@ -407,7 +407,26 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 const int s = g & 1;
                 const bool tail = p.mode == 1 && rows < C;
                 const uint32_t v = smem_u32(sm + OFF_V + s * PANEL);
-                if (!state_only) {
+                if (!tc::warp_wait(&v_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
+                if (tail) {
+                    // rows past the end of a packed sequence hold another one's tokens,
+                    // or anything: cleared in V and K, since 0 x NaN is not 0 (Q K^T may
+                    // read them either way: those columns of P are masked)
+                    if (!tc::warp_wait(&k_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
+                    clear_rows(v, rows, t);
+#pragma unroll 1
+                    for (int pn = 0; pn < NP; ++pn) clear_rows(smem_u32(sm + OFF_K + s * TILE + pn * PANEL), rows, t);
+                }
+                // --- V terms of the first half of the rows
+                if (!rev && rows < C) w.set<rev>(power, lam16, r0, rows);
+                if (g > 0 && !tc::warp_wait(&vt_empty[0], (g - 1) & 1, abort, p.status)) { stop = true; break; }
+                v_terms(v + static_cast<uint32_t>(t) * 16u, smem_u32(sm + OFF_VT) + static_cast<uint32_t>(t) * 16u, w, r0, rows, tail);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&vt_full[0]);
+                    mbar_arrive(state_only ? &v_empty[s] : &v_read[s]);
+                }
+                if (state_only) continue;
                 const uint32_t tp = tlane + TM_P + 128u * s;
                 if (!tc::warp_wait(&p_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
                 tc_fence_after();
@@ -453,35 +472,8 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                // P V also needs V; rows past the end of a packed sequence hold
-                // another one's tokens, or anything: cleared, since 0 x NaN is not 0
-                if (!tc::warp_wait(&v_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
-                if (tail) {
-                    clear_rows(v, rows, t);
-                    fence_proxy_async_smem();
-                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[s]);
-                } else if (!tc::warp_wait(&v_full[s], (g >> 1) & 1, abort, p.status)) {
-                    stop = true;
-                    break;
-                }
-                // --- V terms of the first half of the rows
-                if (!rev && rows < C) w.set<rev>(power, lam16, r0, rows);
-                if (tail) {
-                    // K rows past the end: cleared too (Q K^T may read them either way:
-                    // those columns of P are masked)
-                    if (!tc::warp_wait(&k_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
-#pragma unroll 1
-                    for (int pn = 0; pn < NP; ++pn) clear_rows(smem_u32(sm + OFF_K + s * TILE + pn * PANEL), rows, t);
-                }
-                if (g > 0 && !tc::warp_wait(&vt_empty[0], (g - 1) & 1, abort, p.status)) { stop = true; break; }
-                v_terms(v + static_cast<uint32_t>(t) * 16u, smem_u32(sm + OFF_VT) + static_cast<uint32_t>(t) * 16u, w, r0, rows, tail);
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&vt_full[0]);
-                    mbar_arrive(state_only ? &v_empty[s] : &v_read[s]);
-                }
             }
         }
     } else if (warp < 10) {
@@ -491,6 +483,8 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const bool own = KD == 128 || q4 < KD / 32;  // warp-uniform; at d = 64 warps 8, 9 only follow along
         const uint32_t tds = tbase + (static_cast<uint32_t>(q4 * 32) << 16) + TM_DS;
         const uint32_t srow = smem_u32(sm + OFF_S) + static_cast<uint32_t>(i) * 128u;
+        const int t = (warp - 6) * 32 + lane;
+        const int r0 = 64 + (t >> 3);  // first row of its V terms
         int g = 0;
         bool stop = false;
         for (int r = 0; !stop; ++r) {
@@ -514,12 +508,30 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
                 for (int j = 0; j < DVS / 2; ++j) S[j] = 0ull;
             }
-            float2 lam = item_power(p, it.c1, it.c2, C);  // lam^R
+            auto power = [&](int n) { return item_power(p, it.c1, it.c2, n); };
+            const float2 step = power(16);
+            const double lam16 = static_cast<double>(step.x) + step.y;
+            Weights w;
+            w.set<rev>(power, lam16, r0, C);
+            float2 lam = power(C);  // lam^R
             const int nc = (it.len + C - 1) / C;
             // a sequence's one chunk of other than C rows: its last (in reverse
             // order the first visited)
             const int odd = it.len % C, odd_at = odd ? (rev ? 0 : nc - 1) : -1;
             for (int c = 0; c < nc; ++c, ++g) {
+                const int rows = c == odd_at ? odd : C;
+                const int s = g & 1;
+                // --- V terms of the second half of the rows
+                if (!rev && rows < C) w.set<rev>(power, lam16, r0, rows);
+                if (!tc::warp_wait(&v_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
+                if (g > 0 && !tc::warp_wait(&vt_empty[1], (g - 1) & 1, abort, p.status)) { stop = true; break; }
+                v_terms(smem_u32(sm + OFF_V + s * PANEL) + static_cast<uint32_t>(512 + t) * 16u,
+                        smem_u32(sm + OFF_VT) + static_cast<uint32_t>(512 + t) * 16u, w, r0, rows, p.mode == 1 && rows < C);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&vt_full[1]);
+                    mbar_arrive(state_only ? &v_empty[s] : &v_read[s]);
+                }
                 if (!state_only) {
                     // publish bf16(S) once Q S of the chunk before has read the old one
                     if (g > 0 && !tc::warp_wait(o_full, (g - 1) & 1, abort, p.status)) { stop = true; break; }
@@ -533,7 +545,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_full);
                 }
-                if (c == odd_at) lam = item_power(p, it.c1, it.c2, odd);
+                if (c == odd_at) lam = power(odd);
                 const uint64_t fh = f32x2(lam.x, lam.x), fl = f32x2(lam.y, lam.y);
                 if (!tc::warp_wait(ds_full, g & 1, abort, p.status)) { stop = true; break; }
                 tc_fence_after();
@@ -554,7 +566,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ds_empty);
-                if (rev && c == odd_at) lam = item_power(p, it.c1, it.c2, C);
+                if (rev && c == odd_at) lam = power(C);
             }
             if (stop) break;
             if (p.s_out && it.write_state && own) {
@@ -572,45 +584,26 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // ------------------------------------------------------ output warps
         const int q4 = warp & 3;
         const int row = q4 * 32 + lane;
-        const int t = (warp - 10) * 32 + lane;
-        const int r0 = 64 + (t >> 3);  // first row of its V terms
         const uint32_t tlane = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
         int g = 0;
         int pending = -1;  // V slot whose O store may still be reading it
-        bool stop = false;
+        bool stop = state_only;
         for (int r = 0; !stop; ++r) {
             const int idx = tc::item_index(r, cta, G);
             if (idx >= p.n_items) break;
             const tc::Item it = item<KD>(p, idx);
             const int nc = (it.len + C - 1) / C;
             const float g2 = p.log_decay[p.mode == 0 ? it.c2 % p.H : it.c1] * 1.4426950408889634f;
-            auto power = [&](int n) { return item_power(p, it.c1, it.c2, n); };
-            const float2 step = power(16);
-            const double lam16 = static_cast<double>(step.x) + step.y;
-            Weights w;
-            w.set<rev>(power, lam16, r0, C);
             for (int c = 0; c < nc; ++c, ++g) {
                 const int c0 = tc::chunk_row(rev, c, nc);
                 const int rows = min(C, it.len - c0);
                 const int s = g & 1;
-                // --- V terms of the second half of the rows
-                if (!rev && rows < C) w.set<rev>(power, lam16, r0, rows);
-                if (!tc::warp_wait(&v_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
-                if (g > 0 && !tc::warp_wait(&vt_empty[1], (g - 1) & 1, abort, p.status)) { stop = true; break; }
-                v_terms(smem_u32(sm + OFF_V + s * PANEL) + static_cast<uint32_t>(512 + t) * 16u,
-                        smem_u32(sm + OFF_VT) + static_cast<uint32_t>(512 + t) * 16u, w, r0, rows, p.mode == 1 && rows < C);
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&vt_full[1]);
-                    mbar_arrive(state_only ? &v_empty[s] : &v_read[s]);
-                    // the chunk before has been stored from its V slot
-                    if (pending >= 0) {
-                        bulk_wait_read<0>();
-                        mbar_arrive(&v_empty[pending]);
-                    }
+                // the chunk before has been stored from its V slot
+                if (lane == 0 && pending >= 0) {
+                    bulk_wait_read<0>();
+                    mbar_arrive(&v_empty[pending]);
                 }
-                if (state_only) continue;
-                // --- O
+                __syncwarp();
                 // lam^n of this row (rounded to bf16 with the output: a plain fp32
                 // power will do)
                 const int n = rev ? max(rows - 1 - row, 0) : row + 1;
