@@ -52,6 +52,22 @@ def _stream(device: torch.device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return None
+
+
+_HERE = _Here()
+
+
+def _on(device: torch.device):
+    """The tensors' device made current for a call (nothing to do, and no time spent, when it already is)."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
 def _need(t: torch.Tensor, name: str, dtype=None, device=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -355,7 +371,7 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, S: torch.Tens
         _check_decay(log_decay, H, q.device, phi)
         if tuple(out.shape) != (B, H, dv):
             raise ValueError("out must be [B, H, dv]")
-        with torch.cuda.device(q.device):
+        with _on(q.device):
             _abi.check(lib.la_decode_step_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(S), _ptr(log_decay), B, H,
                                                 dk, dv, _dtype_code(q), _STATE_DT[S.dtype], _stream(q.device)),
                        "la_decode_step_decay")
@@ -413,23 +429,25 @@ def decode_commit(k: torch.Tensor, v: torch.Tensor, S: torch.Tensor, accepted: t
 
 def _heads_view(t: torch.Tensor, name: str, dtype, device):
     """la_view of heads [B, H, N, d] or packed [T, H, d] (one batch entry), last dim contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.numel() and t.stride(-1) != 1:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1 and t.numel():
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # the stride of a dimension of one entry (or none) says nothing
-    st = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
-    b, h, n = st if t.dim() == 4 else (0, st[1], st[0])
-    return _abi.View(t.data_ptr(), b, h, n)
+    if len(st) == 4:
+        return _abi.View(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0,
+                         st[2] if shape[2] > 1 else 0)
+    return _abi.View(t.data_ptr(), 0, st[1] if shape[1] > 1 else 0, st[0] if shape[0] > 1 else 0)
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, inv_freq, positions):
     """Checks of the arguments that both directions share; returns (B, N, Hq, Hk, d, positions' pointer, their
     width, strides, the weights' dtype code)."""
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
     if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape[-1] != q.shape[-1]:
         raise ValueError("q and k must be [B, H, N, d], or packed [T, H, d]")
     if q.dim() == 4:
@@ -494,7 +512,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
         raise ValueError("q_out and k_out must have the shapes of q and k")
     views = [_heads_view(t, n, q.dtype, q.device)
              for t, n in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))]
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         _abi.check(lib.la_qk_norm_rope(*views, _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), pos64,
                                        psb, psn, B, N, Hq, Hk, d, rot, eps, int(interleaved), dt, wdt,
                                        _stream(q.device)), "la_qk_norm_rope")
@@ -522,7 +540,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     views = [_heads_view(t, n, q.dtype, q.device) for t, n in
              ((dq_out, "dq_out"), (dk_out, "dk_out"), (q, "q"), (k, "k"), (dq, "dq"), (dk, "dk"))]
     dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         need = int(lib.la_qk_norm_rope_backward_workspace_size(d))
         if workspace is None or workspace.numel() * workspace.element_size() < need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

@@ -9,13 +9,13 @@
 // g = R(-p) dy:
 //   dx = r (w g - xh mean(w g xh)),   dw = sum over tokens and heads of g xh.
 //
-// Bound by the bytes of q and k: a row (one head of one token, d values) is
-// held by LPR = d sizeof(T) / 16 lanes with one 16-byte vector each; statistics
-// are fp32 sums over those lanes, the partner of a pair sits in another lane
-// of the row (or in the same vector when interleaved).  A block of 256 threads
-// takes ROWS consecutive rows in (token, head) order, every thread's loads
-// issued before any use, and forms the cosines and sines of its tokens once in
-// shared memory meanwhile.
+// Bound by the bytes of q and k.  A row (one head of one token, d values) is
+// held by d / (2 VEC) lanes with two 16-byte vectors each; with pairs (i, i +
+// rot/2) a lane's two vectors are the two halves of its pairs, so that the
+// rotation needs no exchange between lanes.  A block takes consecutive rows of q
+// or of k in (token, head) order, every thread's loads issued before any use,
+// and forms the cosines and sines of its tokens once in shared memory meanwhile;
+// its weights stay in registers.
 //
 // Angles: p f is formed in double, in turns, and reduced to [-1/2, 1/2] before
 // it is rounded to fp32 for sincospi: a position of 2^20 is 10^5 radians, where
@@ -28,30 +28,34 @@
 namespace lcl {
 namespace nrope {
 
-constexpr int NUM_THREADS = 256;
-constexpr int UNROLL = 4;  // rows per thread and pass
+constexpr int NUM_THREADS = 128;  // (256: 211 instead of 199 us forward, 356 instead of 349 backward at the size below)
 
 struct View {
     const void* p;
     long sb, sh, sn;  // strides in elements
 };
 
+struct Side {         // q or k
+    View x;
+    View dy;          // backward: gradient of the output
+    View y;           // output (backward: gradient of x)
+    const void* w;
+    long rows;        // B * N * H
+    int H;
+    int blocks;
+};
+
 struct Params {
-    View x[2];        // q, k
-    View dy[2];       // backward: gradients of the outputs
-    View y[2];        // outputs (backward: gradients of q, k)
-    const void* w[2];
+    Side side[2];     // blocks of q first
     int w32;          // weights are fp32 (else the element type)
-    int Hq, HT;       // query heads, query + key heads
-    long N;           // tokens per batch entry
-    long rows;        // B * N * HT
+    int N;            // tokens per batch entry
     const void* pos;  // int32 or int64, or null (token index n)
     int pos64;
     long pos_sb, pos_sn;
     const float* inv_freq;
     int half;         // rot / 2
     float eps;
-    float* partial;   // backward: [gridDim.x][2][d]
+    float* partial;   // backward: [blocks][d]
 };
 
 template <typename T> struct Elem;
@@ -85,25 +89,76 @@ template <> struct Elem<__nv_bfloat16> {
     }
 };
 
-template <typename T, int D> constexpr int lanes_per_row() { return D / Elem<T>::VEC; }
-// rows per block and pass
-template <typename T, int D> constexpr int block_rows() { return NUM_THREADS / lanes_per_row<T, D>() * UNROLL; }
-// most tokens that a block's rows belong to
-template <typename T, int D> int block_tokens(int HT) { return (block_rows<T, D>() + HT - 2) / HT + 1; }
+template <typename T, int D> constexpr int lanes_per_row() { return D / Elem<T>::VEC / 2; }
+// rows per block and pass, U of them per thread
+template <typename T, int D, int U> constexpr int block_rows() { return NUM_THREADS / lanes_per_row<T, D>() * U; }
+// most tokens that `rows` consecutive rows of H heads belong to
+inline int block_tokens(int rows, int H) { return (rows + H - 2) / H + 1; }
+
+// A block's rows in (token, head) order, from one division by H per block:
+// everything per row is 32-bit.  (With 64-bit divisions per row the first
+// version spent most of its instructions on them.)
+struct Rows {
+    long b0;     // batch entry of the first row
+    int n0, h0;  // its token within the entry, its head
+};
+__device__ __forceinline__ Rows first_row(int N, int H, long row0) {
+    Rows r;
+    if (row0 < (1l << 31)) {
+        const unsigned row = static_cast<unsigned>(row0), tok = row / static_cast<unsigned>(H);
+        r.h0 = static_cast<int>(row - tok * H);
+        const unsigned b = tok / static_cast<unsigned>(N);
+        r.n0 = static_cast<int>(tok - b * N);
+        r.b0 = b;
+    } else {
+        const long tok = row0 / H;
+        r.h0 = static_cast<int>(row0 - tok * H);
+        r.b0 = tok / N;
+        r.n0 = static_cast<int>(tok - r.b0 * N);
+    }
+    return r;
+}
+// Token tt after the block's first one: batch entry and token within it.
+__device__ __forceinline__ void token_at(const Rows& r, int N, int tt, long& b, int& n) {
+    const unsigned nn = static_cast<unsigned>(r.n0 + tt);
+    const unsigned over = nn < static_cast<unsigned>(N) ? 0u : nn / static_cast<unsigned>(N);
+    b = r.b0 + over;
+    n = static_cast<int>(nn - over * N);
+}
+// Row i of the block: its token's distance from the first one, and where it is.
+struct At {
+    int tt, h, n;
+    long b;
+    __device__ __forceinline__ long in(const View& v) const { return b * v.sb + h * v.sh + n * v.sn; }
+};
+__device__ __forceinline__ At row_at(const Rows& r, int N, int H, int i) {
+    At a;
+    const unsigned h = static_cast<unsigned>(r.h0 + i);
+    a.tt = h < static_cast<unsigned>(H) ? 0 : static_cast<int>(h / static_cast<unsigned>(H));
+    a.h = static_cast<int>(h) - a.tt * H;
+    token_at(r, N, a.tt, a.b, a.n);
+    return a;
+}
 
 __device__ __forceinline__ float row_sum(float s, int lpr) {
     for (int o = lpr >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
 
-// cos and sin of position * inv_freq for `tokens` tokens from token tok0 on
-__device__ __forceinline__ void fill_angles(const Params& p, long tok0, int tokens, long all_tokens, float2* cs) {
+// cos and sin of position * inv_freq for the tokens of the block's `rows` rows.
+// A lane reads the F frequencies of its vector as F / 2 float4s; the i-th float4
+// of every vector lie side by side, so that lanes read neighbouring ones
+// (frequency by frequency their stride was F x 8 bytes: four-way bank conflicts,
+// 16 % of the pass).
+template <int F>
+__device__ __forceinline__ void fill_angles(const Params& p, const Rows& r, int H, int rows, float2* cs) {
     constexpr double INV_2PI = 0.15915494309189533576888;
+    const int tokens = (r.h0 + rows - 1) / H + 1;
     for (int e = threadIdx.x; e < tokens * p.half; e += NUM_THREADS) {
         const int tt = e / p.half, i = e - tt * p.half;
-        const long tok = tok0 + tt;
-        if (tok >= all_tokens) break;
-        const long b = tok / p.N, n = tok - b * p.N;
+        long b;
+        int n;
+        token_at(r, p.N, tt, b, n);
         double pos;
         if (!p.pos) pos = static_cast<double>(n);
         else if (p.pos64) pos = static_cast<double>(reinterpret_cast<const long long*>(p.pos)[b * p.pos_sb + n * p.pos_sn]);
@@ -111,205 +166,257 @@ __device__ __forceinline__ void fill_angles(const Params& p, long tok0, int toke
         const double turns = pos * (static_cast<double>(p.inv_freq[i]) * INV_2PI);
         float s, c;
         sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-        cs[e] = make_float2(c, s);
+        cs[tt * p.half + ((i % F) / 2 * (p.half / F) + i / F) * 2 + (i & 1)] = make_float2(c, s);
     }
 }
 
-// The row's vector turned by its token's angles (sgn = 1) or back (sgn = -1);
-// every lane of the warp takes part.
+// The two vectors (indices in units of VEC values) of lane l of a row.  With
+// pairs (i, i + half): lane l < half / VEC holds the l-th vector of either half,
+// the others the vectors behind them, which are not turned.  Interleaved: l
+// and l + LPR (a row's 16-byte loads then cover whole 128-byte lines).
 template <int VEC, int LPR, bool kInter>
-__device__ __forceinline__ void rotate(float (&f)[VEC], const float2* cs, int lane, int half, float sgn) {
+__device__ __forceinline__ void lane_vectors(int l, int half, int (&vec)[2]) {
     if constexpr (kInter) {
-        if (lane * VEC < 2 * half) {
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) {
-                const float2 t = cs[lane * (VEC / 2) + i];
-                const float a = f[2 * i], b = f[2 * i + 1], s = sgn * t.y;
-                f[2 * i] = a * t.x - b * s;
-                f[2 * i + 1] = b * t.x + a * s;
-            }
-        }
+        vec[0] = l;
+        vec[1] = l + LPR;
     } else {
         const int hl = half / VEC;
-        const bool first = lane < hl, turned = lane < 2 * hl;
-        const int partner = !turned ? lane : (first ? lane + hl : lane - hl);
-        const float2* t = cs + (first ? lane : lane - hl) * VEC;
-        const float ss = first ? -sgn : sgn;
+        vec[0] = l < hl ? l : 2 * l;
+        vec[1] = l < hl ? l + hl : 2 * l + 1;
+    }
+}
+
+// A lane's 2 VEC values turned by their token's angles (sgn = 1) or back (-1).
+template <int VEC, int LPR, bool kInter>
+__device__ __forceinline__ void rotate(float (&f)[2][VEC], const float2* cs, int l, int half, float sgn) {
+    if constexpr (kInter) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float other = __shfl_sync(0xffffffffu, f[i], partner, LPR);
-            if (turned) f[i] = f[i] * t[i].x + other * (ss * t[i].y);
+        for (int v = 0; v < 2; ++v) {
+            const int e0 = (l + v * LPR) * VEC;
+            if (e0 < 2 * half) {
+                const float4* t = reinterpret_cast<const float4*>(cs) + l + v * LPR;
+#pragma unroll
+                for (int i = 0; i < VEC / 4; ++i) {
+                    const float4 x = t[i * (2 * half / VEC)];  // cos, sin of two pairs
+                    float a = f[v][4 * i], b = f[v][4 * i + 1];
+                    f[v][4 * i] = a * x.x - b * (sgn * x.y);
+                    f[v][4 * i + 1] = b * x.x + a * (sgn * x.y);
+                    a = f[v][4 * i + 2], b = f[v][4 * i + 3];
+                    f[v][4 * i + 2] = a * x.z - b * (sgn * x.w);
+                    f[v][4 * i + 3] = b * x.z + a * (sgn * x.w);
+                }
+            }
+        }
+    } else if (l * VEC < half) {
+        const float4* t = reinterpret_cast<const float4*>(cs) + l;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const float4 x = t[i * (half / VEC)];
+            float a = f[0][2 * i], b = f[1][2 * i];
+            f[0][2 * i] = a * x.x - b * (sgn * x.y);
+            f[1][2 * i] = b * x.x + a * (sgn * x.y);
+            a = f[0][2 * i + 1], b = f[1][2 * i + 1];
+            f[0][2 * i + 1] = a * x.z - b * (sgn * x.w);
+            f[1][2 * i + 1] = b * x.z + a * (sgn * x.w);
         }
     }
 }
 
-template <int VEC, typename T>
-__device__ __forceinline__ void load_weight(const Params& p, int side, int lane, float (&w)[VEC]) {
+template <typename T>
+__device__ __forceinline__ void load_weight(const Params& p, const void* weight, int vec, float (&w)[Elem<T>::VEC]) {
+    constexpr int VEC = Elem<T>::VEC;
     if (p.w32) {
-        const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.w[side]) + lane * VEC);
+        const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(weight) + vec * VEC);
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i) {
             const float4 x = __ldg(src + i);
             w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
         }
     } else {
-        Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w[side]) + lane * VEC)), w);
+        Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + vec * VEC)), w);
     }
 }
 
-template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(NUM_THREADS)
+// U rows per thread: 4 for many rows (bytes in flight), 1 for few.  4 x 8192
+// tokens of 32 + 32 bf16 heads of 128, from the projection's layout to the
+// attention's, all dims turned: 0.199 ms, 5.4 TB/s = 0.83 of a copy (norm alone
+// 0.188); 2 rows per thread 0.208.
+template <typename T, int D, bool kInter, int U>
+__global__ void __launch_bounds__(NUM_THREADS, 6)
 norm_rope_kernel(const __grid_constant__ Params p) {
-    constexpr int VEC = Elem<T>::VEC, LPR = lanes_per_row<T, D>(), RB = NUM_THREADS / LPR, ROWS = RB * UNROLL;
-    extern __shared__ float2 cs[];
+    constexpr int VEC = Elem<T>::VEC, LPR = lanes_per_row<T, D>(), RB = NUM_THREADS / LPR, ROWS = RB * U;
+    extern __shared__ float4 cs4[];
+    float2* cs = reinterpret_cast<float2*>(cs4);
+    const bool second = static_cast<int>(blockIdx.x) >= p.side[0].blocks;
+    const Side& sd = p.side[second];
     const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    const long row0 = static_cast<long>(blockIdx.x) * ROWS;
-    const long tok0 = row0 / p.HT;
-    uint4 r[UNROLL];
+    const long row0 = static_cast<long>(blockIdx.x - (second ? p.side[0].blocks : 0)) * ROWS;
+    const int rows = static_cast<int>(min(static_cast<long>(ROWS), sd.rows - row0));
+    const Rows first = first_row(p.N, sd.H, row0);
+    int vec[2];
+    lane_vectors<VEC, LPR, kInter>(lane, p.half, vec);
+    uint4 r[U][2];
+    long out[U];
+    int tt[U];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-        const long row = row0 + slot + u * RB;
-        r[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < p.rows) {
-            const long tok = row / p.HT;
-            const int h = static_cast<int>(row - tok * p.HT), side = h >= p.Hq, hs = side ? h - p.Hq : h;
-            const long b = tok / p.N, n = tok - b * p.N;
-            const View& x = p.x[side];
-            r[u] = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(x.p) + b * x.sb + hs * x.sh + n * x.sn +
-                                                         lane * VEC));
-        }
+    for (int u = 0; u < U; ++u) {
+        const int i = slot + u * RB;
+        const At at = row_at(first, p.N, sd.H, i < rows ? i : 0);
+        const T* src = reinterpret_cast<const T*>(sd.x.p) + at.in(sd.x);
+        out[u] = at.in(sd.y);
+        tt[u] = at.tt;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            r[u][v] = i < rows ? __ldcs(reinterpret_cast<const uint4*>(src + vec[v] * VEC)) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (p.half) {
-        const long last = min(row0 + ROWS, p.rows) - 1;
-        fill_angles(p, tok0, static_cast<int>(last / p.HT - tok0) + 1, p.rows / p.HT, cs);
-    }
+    if (p.half) fill_angles<kInter ? VEC / 2 : VEC>(p, first, sd.H, rows, cs);
+    float w[2][VEC];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) load_weight<T>(p, sd.w, vec[v], w[v]);
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-        const long row = row0 + slot + u * RB;
-        const bool live = row < p.rows;
-        const long tok = (live ? row : row0) / p.HT;
-        const int h = live ? static_cast<int>(row - tok * p.HT) : 0, side = h >= p.Hq, hs = side ? h - p.Hq : h;
-        float f[VEC], w[VEC];
-        Elem<T>::unpack(r[u], f);
+    for (int u = 0; u < U; ++u) {
+        float f[2][VEC];
         float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) ss = fmaf(f[i], f[i], ss);
-        const float rs = rsqrtf(row_sum(ss, LPR) * (1.f / D) + p.eps);
-        load_weight<VEC, T>(p, side, lane, w);
+        for (int v = 0; v < 2; ++v) {
+            Elem<T>::unpack(r[u][v], f[v]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] = f[i] * rs * w[i];
-        if (p.half) rotate<VEC, LPR, kInter>(f, cs + (tok - tok0) * p.half, lane, p.half, 1.f);
-        if (live) {
-            const long b = tok / p.N, n = tok - b * p.N;
-            const View& y = p.y[side];
-            T* dst = reinterpret_cast<T*>(const_cast<void*>(y.p)) + b * y.sb + hs * y.sh + n * y.sn + lane * VEC;
-            *reinterpret_cast<uint4*>(dst) = Elem<T>::pack(f);
+            for (int i = 0; i < VEC; ++i) ss = fmaf(f[v][i], f[v][i], ss);
+        }
+        const float rs = rsqrtf(row_sum(ss, LPR) * (1.f / D) + p.eps);
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[v][i] = f[v][i] * rs * w[v][i];
+        rotate<VEC, LPR, kInter>(f, cs + tt[u] * p.half, lane, p.half, 1.f);
+        if (slot + u * RB < rows) {
+            T* dst = reinterpret_cast<T*>(const_cast<void*>(sd.y.p)) + out[u];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) *reinterpret_cast<uint4*>(dst + vec[v] * VEC) = Elem<T>::pack(f[v]);
         }
     }
 }
 
-// Gradients of q and k, and per block the sums of g xh over its rows (fixed
-// order: a block's rows depend on the grid alone).
-template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(NUM_THREADS)
+// Gradients of q or k, and per block the sums of g xh over its rows (fixed
+// order: a block's rows depend on the grid alone).  The same size: 0.349 ms,
+// 4.6 TB/s = 0.70 of a copy: 32 accumulators and weights leave 128 registers and
+// 16 warps per SM, whose loads and arithmetic overlap across blocks only
+// (1 row per thread 0.44, fewer blocks per SM 0.39).
+template <typename T, int D, bool kInter, int U>
+__global__ void __launch_bounds__(NUM_THREADS, 4)
 norm_rope_backward_kernel(const __grid_constant__ Params p) {
-    constexpr int VEC = Elem<T>::VEC, LPR = lanes_per_row<T, D>(), RB = NUM_THREADS / LPR, ROWS = RB * UNROLL;
-    extern __shared__ float2 cs[];
-    __shared__ float red[2][RB][D];
+    constexpr int VEC = Elem<T>::VEC, LPR = lanes_per_row<T, D>(), RB = NUM_THREADS / LPR, ROWS = RB * U;
+    constexpr int WARPS = NUM_THREADS / 32;
+    extern __shared__ float4 cs4[];
+    float2* cs = reinterpret_cast<float2*>(cs4);
+    __shared__ float red[WARPS][D];
+    const bool second = static_cast<int>(blockIdx.x) >= p.side[0].blocks;
+    const Side& sd = p.side[second];
     const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    float dw[2][VEC];
+    int vec[2];
+    lane_vectors<VEC, LPR, kInter>(lane, p.half, vec);
+    float w[2][VEC], dw[2][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) dw[0][i] = dw[1][i] = 0.f;
-    for (long row0 = static_cast<long>(blockIdx.x) * ROWS; row0 < p.rows; row0 += static_cast<long>(gridDim.x) * ROWS) {
-        const long tok0 = row0 / p.HT;
-        uint4 rx[UNROLL], rd[UNROLL];
+    for (int v = 0; v < 2; ++v) {
+        load_weight<T>(p, sd.w, vec[v], w[v]);
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const long row = row0 + slot + u * RB;
-            rx[u] = rd[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < p.rows) {
-                const long tok = row / p.HT;
-                const int h = static_cast<int>(row - tok * p.HT), side = h >= p.Hq, hs = side ? h - p.Hq : h;
-                const long b = tok / p.N, n = tok - b * p.N;
-                const View &x = p.x[side], &d = p.dy[side];
-                rx[u] = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(x.p) + b * x.sb + hs * x.sh +
-                                                              n * x.sn + lane * VEC));
-                rd[u] = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(d.p) + b * d.sb + hs * d.sh +
-                                                              n * d.sn + lane * VEC));
+        for (int i = 0; i < VEC; ++i) dw[v][i] = 0.f;
+    }
+    for (long row0 = static_cast<long>(blockIdx.x - (second ? p.side[0].blocks : 0)) * ROWS; row0 < sd.rows;
+         row0 += static_cast<long>(sd.blocks) * ROWS) {
+        const int rows = static_cast<int>(min(static_cast<long>(ROWS), sd.rows - row0));
+        const Rows first = first_row(p.N, sd.H, row0);
+        uint4 rx[U][2], rd[U][2];
+        long out[U];
+        int tt[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = slot + u * RB;
+            const At at = row_at(first, p.N, sd.H, i < rows ? i : 0);
+            const T* x = reinterpret_cast<const T*>(sd.x.p) + at.in(sd.x);
+            const T* d = reinterpret_cast<const T*>(sd.dy.p) + at.in(sd.dy);
+            out[u] = at.in(sd.y);
+            tt[u] = at.tt;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                rx[u][v] = i < rows ? __ldcs(reinterpret_cast<const uint4*>(x + vec[v] * VEC)) : make_uint4(0u, 0u, 0u, 0u);
+                rd[u][v] = i < rows ? __ldcs(reinterpret_cast<const uint4*>(d + vec[v] * VEC)) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        __syncthreads();  // the angles of the previous pass have been read
-        if (p.half) {
-            const long last = min(row0 + ROWS, p.rows) - 1;
-            fill_angles(p, tok0, static_cast<int>(last / p.HT - tok0) + 1, p.rows / p.HT, cs);
-        }
+        __syncthreads();  // the angles of the pass before have been read
+        if (p.half) fill_angles<kInter ? VEC / 2 : VEC>(p, first, sd.H, rows, cs);
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const long row = row0 + slot + u * RB;
-            const bool live = row < p.rows;
-            const long tok = (live ? row : row0) / p.HT;
-            const int h = live ? static_cast<int>(row - tok * p.HT) : 0, side = h >= p.Hq, hs = side ? h - p.Hq : h;
-            float f[VEC], g[VEC], w[VEC];
-            Elem<T>::unpack(rx[u], f);
-            Elem<T>::unpack(rd[u], g);
+        for (int u = 0; u < U; ++u) {
+            const bool live = slot + u * RB < rows;
+            float f[2][VEC], g[2][VEC];
             float ss = 0.f;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) ss = fmaf(f[i], f[i], ss);
+            for (int v = 0; v < 2; ++v) {
+                Elem<T>::unpack(rx[u][v], f[v]);
+                Elem<T>::unpack(rd[u][v], g[v]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) ss = fmaf(f[v][i], f[v][i], ss);
+            }
             const float rs = rsqrtf(row_sum(ss, LPR) * (1.f / D) + p.eps);
-            if (p.half) rotate<VEC, LPR, kInter>(g, cs + (tok - tok0) * p.half, lane, p.half, -1.f);
-            load_weight<VEC, T>(p, side, lane, w);
+            rotate<VEC, LPR, kInter>(g, cs + tt[u] * p.half, lane, p.half, -1.f);
             float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                f[i] *= rs;  // xh
-                const float gx = live ? g[i] * f[i] : 0.f;
-                if (side) dw[1][i] += gx;
-                else dw[0][i] += gx;
-                w[i] *= g[i];
-                dot = fmaf(w[i], f[i], dot);
-            }
-            dot = row_sum(dot, LPR) * (1.f / D);
+            for (int v = 0; v < 2; ++v)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = rs * (w[i] - f[i] * dot);
+                for (int i = 0; i < VEC; ++i) {
+                    f[v][i] *= rs;  // xh
+                    if (live) dw[v][i] = fmaf(g[v][i], f[v][i], dw[v][i]);
+                    g[v][i] *= w[v][i];
+                    dot = fmaf(g[v][i], f[v][i], dot);
+                }
+            dot = row_sum(dot, LPR) * (1.f / D);
             if (live) {
-                const long b = tok / p.N, n = tok - b * p.N;
-                const View& y = p.y[side];
-                T* dst = reinterpret_cast<T*>(const_cast<void*>(y.p)) + b * y.sb + hs * y.sh + n * y.sn + lane * VEC;
-                *reinterpret_cast<uint4*>(dst) = Elem<T>::pack(f);
+                T* dst = reinterpret_cast<T*>(const_cast<void*>(sd.y.p)) + out[u];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) f[v][i] = rs * (g[v][i] - f[v][i] * dot);
+                    *reinterpret_cast<uint4*>(dst + vec[v] * VEC) = Elem<T>::pack(f[v]);
+                }
             }
         }
     }
+    // the rows of a warp, then of the block
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        red[0][slot][lane * VEC + i] = dw[0][i];
-        red[1][slot][lane * VEC + i] = dw[1][i];
-    }
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            float s = dw[v][i];
+            for (int o = LPR; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (threadIdx.x % 32 < LPR) red[threadIdx.x / 32][vec[v] * VEC + i] = s;
+        }
     __syncthreads();
-    for (int e = threadIdx.x; e < 2 * D; e += NUM_THREADS) {
-        const int side = e / D, i = e - side * D;
+    for (int e = threadIdx.x; e < D; e += NUM_THREADS) {
         float s = 0.f;
-        for (int r = 0; r < RB; ++r) s += red[side][r][i];
-        p.partial[static_cast<long>(blockIdx.x) * 2 * D + e] = s;
+        for (int k = 0; k < WARPS; ++k) s += red[k][e];
+        p.partial[static_cast<long>(blockIdx.x) * D + e] = s;
     }
 }
 
-// dw = sum of the blocks' partial sums, [blocks][2][d] -> dq_weight, dk_weight:
-// 32 columns per block, 8 warps over the partial rows, joined in a fixed order.
+// dw = sum of the blocks' partial sums [blocks_q + blocks_k][d]: block (x, side)
+// takes 32 columns, 4 warps over the partial rows, joined in a fixed order.
 __global__ void __launch_bounds__(NUM_THREADS)
-weight_grad_kernel(const float* __restrict__ partial, int blocks, int d, float* __restrict__ dwq, float* __restrict__ dwk) {
-    __shared__ float red[8][32];
+weight_grad_kernel(const float* __restrict__ partial, int blocks_q, int blocks_k, int d, float* __restrict__ dwq,
+                   float* __restrict__ dwk) {
+    __shared__ float red[4][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
+    const int b0 = blockIdx.y ? blocks_q : 0, b1 = blockIdx.y ? blocks_q + blocks_k : blocks_q;
+    float* dst = blockIdx.y ? dwk : dwq;
     float s = 0.f;
-    for (int b = warp; b < blocks; b += 8) s += partial[static_cast<long>(b) * 2 * d + col];
+    for (int b = b0 + warp; b < b1; b += 4) s += partial[static_cast<long>(b) * d + col];
     red[warp][lane] = s;
     __syncthreads();
-    if (warp == 0) {
-        for (int w = 1; w < 8; ++w) s += red[w][lane];
-        float* dst = col < d ? dwq : dwk;
-        if (dst) dst[col < d ? col : col - d] = s;
+    if (warp == 0 && dst) {
+        for (int k = 1; k < 4; ++k) s += red[k][lane];
+        dst[col] = s;
     }
 }
 
