@@ -164,10 +164,14 @@ la_status device_info(DeviceInfo** out) {
             (e = set_simt_attrs<__nv_bfloat16, false>()) != cudaSuccess ||
             (e = set_simt_attrs<float, true>()) != cudaSuccess || (e = set_simt_attrs<__nv_bfloat16, true>()) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(prefill_simt)");
-        const void* decay_kernels[4] = {reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, false>),
-                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, true>),
-                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, false>),
-                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, true>)};
+        const void* decay_kernels[8] = {reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, true, false>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, true, false>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, false, true>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, true, true>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, false, false>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, false, true>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, true, true>),
+                                        reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, false, false>)};
         for (const void* kern : decay_kernels)
             if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tcd::SMEM_BYTES)) !=
                 cudaSuccess)
@@ -288,8 +292,14 @@ la_status launch_tc(int grid, const CUtensorMap& mq, const CUtensorMap& mk, cons
     auto go = [&](auto kern) { kern<<<grid, tc::NUM_THREADS, tc::SMEM_BYTES, st>>>(mq, mk, mv, mo, p); };
     if (p.log_decay) {
         auto god = [&](auto kern) { kern<<<grid, tcd::NUM_THREADS, tcd::SMEM_BYTES, st>>>(mq, mk, mv, mo, p); };
-        if (p.dk == 64) p.reverse ? god(tcd::prefill_decay_kernel<64, true>) : god(tcd::prefill_decay_kernel<64, false>);
-        else p.reverse ? god(tcd::prefill_decay_kernel<128, true>) : god(tcd::prefill_decay_kernel<128, false>);
+        const bool lean = p.mode == 0 && !p.state_only;
+        if (p.dk == 64) {
+            if (p.reverse) lean ? god(tcd::prefill_decay_kernel<64, true, true>) : god(tcd::prefill_decay_kernel<64, true, false>);
+            else lean ? god(tcd::prefill_decay_kernel<64, false, true>) : god(tcd::prefill_decay_kernel<64, false, false>);
+        } else {
+            if (p.reverse) lean ? god(tcd::prefill_decay_kernel<128, true, true>) : god(tcd::prefill_decay_kernel<128, true, false>);
+            else lean ? god(tcd::prefill_decay_kernel<128, false, true>) : god(tcd::prefill_decay_kernel<128, false, false>);
+        }
     } else if (p.dk == 64) {
         if (phi) go(tc::prefill_tc_kernel<true, true, 64>);
         else if (general) go(tc::prefill_tc_kernel<true, false, 64>);

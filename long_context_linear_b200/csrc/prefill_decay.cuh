@@ -26,11 +26,12 @@
 // it shares.  In reverse order rows take lam^(m-l) and lam^(R-1-l), the update
 // lam^(m+1) (the state is held already decayed).
 //
-// Shared memory (225 KB): Q 2 x 32 KB, K 2 x 32 KB, V 2 x 16 KB, the three V
-// terms 48 KB (written half of the rows at a time, while the product of the
-// other half runs) and bf16(S) 16 KB, key dims as rows: each state thread
-// writes its row in 16-byte vectors.  O is staged in its chunk's V slot, whose
-// readers are done by then.
+// Shared memory (217 KB): Q 2 x 32 KB, K 2 x 32 KB, V 2 x 16 KB, the three V
+// terms of 32 rows at a time 2 x 12 KB (written while the product of the 32 rows
+// before runs), bf16(S) 16 KB, key dims as rows: each state thread writes its
+// row in 16-byte vectors, and 16 KB to stage O.  (All 128 rows of the terms at
+// once leave no room for that; O staged in its chunk's V slot held the slot for
+// too long: 2.5 us a chunk against 2.3.)
 // TMEM (512 columns): two P buffers of 128 (bf16 P in the first 64 of each,
 // Opv in the others once they have been read), Oqs 64, dS 192.
 //
@@ -43,7 +44,7 @@
 //   w6..w9     : state warps (V terms of rows 64 .. 127, publish bf16(S), absorb dS)
 //   w10..w13   : output warps
 // Q K^T, P and P V need no state and run ahead; the chain from chunk to chunk
-// is terms -> dS -> S -> Q S.  Every wait is bounded (mbar_wait); a timeout
+// is terms -> dS -> S -> Q S.  Every wait is bounded (wait_bounded); a timeout
 // stops the CTA cleanly.
 #pragma once
 #include "decay.cuh"
@@ -62,19 +63,23 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_K = OFF_Q + SLOTS * TILE;
 constexpr int OFF_V = OFF_K + SLOTS * TILE;
 constexpr int OFF_VT = OFF_V + SLOTS * PANEL;
-constexpr int OFF_S = OFF_VT + TERMS * PANEL;
-constexpr int OFF_BAR = OFF_S + PANEL;
-// mbarriers (8 bytes each) at OFF_BAR, then the TMEM base and the abort flag
+constexpr int QROWS = 32;                   // rows of a quarter of the chunk
+constexpr int VT_PANEL = QROWS * 128;       // one term of a quarter
+constexpr int VT_BUF = TERMS * VT_PANEL;
+constexpr int OFF_S = OFF_VT + 2 * VT_BUF;
+constexpr int OFF_OST = OFF_S + PANEL;
+constexpr int OFF_BAR = OFF_OST + PANEL;
+static_assert(OFF_VT % 1024 == 0 && OFF_S % 1024 == 0 && VT_PANEL % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+// mbarriers (8 bytes each) at OFF_BAR, then the TMEM base
 constexpr int BAR_Q_FULL = 0;                      // [2] TMA -> A, C
 constexpr int BAR_Q_EMPTY = BAR_Q_FULL + SLOTS;    // [2] A (Q K^T) + C (Q S) -> TMA
 constexpr int BAR_K_FULL = BAR_Q_EMPTY + SLOTS;    // [2] TMA -> A, B, P warps (ragged tail)
 constexpr int BAR_K_EMPTY = BAR_K_FULL + SLOTS;    // [2] A (Q K^T) + B (dS) -> TMA
 constexpr int BAR_V_FULL = BAR_K_EMPTY + SLOTS;    // [2] TMA -> P warps, state warps
-constexpr int BAR_V_READ = BAR_V_FULL + SLOTS;     // [2] P warps, state warps (terms formed) -> output warps: V may be overwritten
-constexpr int BAR_V_EMPTY = BAR_V_READ + SLOTS;    // [2] output warps (O stored from the slot) -> TMA
-constexpr int BAR_VT_FULL = BAR_V_EMPTY + SLOTS;   // [2] by half of the rows: P warps, state warps -> B
-constexpr int BAR_VT_EMPTY = BAR_VT_FULL + 2;      // [2] by half: B (dS) -> P warps, state warps
-constexpr int BAR_P_FULL = BAR_VT_EMPTY + 2;       // [2] A (Q K^T) -> P warps
+constexpr int BAR_V_EMPTY = BAR_V_FULL + SLOTS;    // [2] P warps, state warps (V read) + C (P V) -> TMA
+constexpr int BAR_VT_FULL = BAR_V_EMPTY + SLOTS;   // [4] by quarter of the rows: P warps (0, 1), state warps (2, 3) -> B
+constexpr int BAR_VT_EMPTY = BAR_VT_FULL + 4;      // [4] by quarter: B (its product done) -> state warps (0, 1), P warps (2, 3)
+constexpr int BAR_P_FULL = BAR_VT_EMPTY + 4;       // [2] A (Q K^T) -> P warps
 constexpr int BAR_P_READY = BAR_P_FULL + 2;        // [2] P warps (bf16 P written, V landed) -> C
 constexpr int BAR_O_FULL = BAR_P_READY + 2;        // C (P V, Q S) -> output warps, state warps
 constexpr int BAR_O_EMPTY = BAR_O_FULL + 1;        // output warps (Opv, Oqs read) -> A, C
@@ -123,16 +128,16 @@ __device__ __forceinline__ void v_split(uint32_t vt, const uint4& r, float w) {
         }
     }
 #pragma unroll
-    for (int n = 0; n < TERMS; ++n) st_shared_v4(vt + n * PANEL, out[n][0], out[n][1], out[n][2], out[n][3]);
+    for (int n = 0; n < TERMS; ++n) st_shared_v4(vt + n * VT_PANEL, out[n][0], out[n][1], out[n][2], out[n][3]);
 }
 
-// The terms of 64 rows of V (half h of the chunk), by 128 threads t: thread t
-// takes the vectors at places t + 128 j of the (swizzled) tile, rows r0 + 16 j;
-// a vector's place in V is its place in every term.
+// A group of 128 threads forms the terms of 64 rows of V, a quarter of 32 rows
+// at a time: thread t takes the vectors at places t + 128 j of the (swizzled)
+// tile, rows r0 + 16 j; a vector's place in V is its place in every term.
 struct Weights {
     float w[4];
-    // rows 64 h + t / 8 + 16 j of a chunk of `rows`, from the smallest exponent
-    // up (rows past the end are zero, whatever their weight)
+    // of rows r0 + 16 j of a chunk of `rows`, from the smallest exponent up (rows
+    // past the end are zero, whatever their weight)
     template <bool kRev, typename F>
     __device__ __forceinline__ void set(const F& power, double lam16, int r0, int rows) {
         const int left = rows - 1 - r0;  // in order: exponent left - 16 j
@@ -146,14 +151,22 @@ struct Weights {
         }
     }
 };
-__device__ __forceinline__ void v_terms(uint32_t v, uint32_t vt, const Weights& w, int r0, int rows, bool tail) {
-    // (rolled: see item())
+// Quarter h (0, 1) of the group's 64 rows, whose places in V start at v.
+// (rolled: see item())
+__device__ __forceinline__ void v_terms(uint32_t v, uint32_t vt, const Weights& w, int h, int r0, int rows, bool tail) {
+    float wa = h ? w.w[2] : w.w[0];
+    const float wb = h ? w.w[3] : w.w[1];
+    r0 += 32 * h;
+    v += static_cast<uint32_t>(h) * VT_PANEL;
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-        uint4 x = ld_shared_v4(v + static_cast<uint32_t>(j) * 2048u);
-        if (tail && r0 + 16 * j >= rows) x = make_uint4(0u, 0u, 0u, 0u);
-        const float wj = j < 2 ? (j == 0 ? w.w[0] : w.w[1]) : (j == 2 ? w.w[2] : w.w[3]);
-        v_split(vt + static_cast<uint32_t>(j) * 2048u, x, wj);
+    for (int j = 0; j < 2; ++j) {
+        uint4 x = ld_shared_v4(v);
+        if (tail && r0 >= rows) x = make_uint4(0u, 0u, 0u, 0u);
+        v_split(vt, x, wa);
+        wa = wb;
+        r0 += 16;
+        v += 2048u;
+        vt += 2048u;
     }
     fence_proxy_async_smem();
 }
@@ -161,6 +174,22 @@ __device__ __forceinline__ void v_terms(uint32_t v, uint32_t vt, const Weights& 
 // Rows rows .. C - 1 of a tile of 128-byte rows set to zero, by 128 threads t.
 __device__ __noinline__ void clear_rows(uint32_t tile, int rows, int t) {
     for (int e = rows * 8 + t; e < C * 8; e += 128) st_shared_v4(tile + static_cast<uint32_t>(e) * 16u, 0u, 0u, 0u, 0u);
+}
+
+// Bounded wait for the phase of the given parity, in few instructions (see
+// item()): up to 100,000 tries, each of which sleeps for up to 20 us or until
+// the phase completes; two seconds in all at most.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 100000;\n\t"
+        "W: mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra D;\n\tsub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra W;\n\t"
+        "D: selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
 }
 
 // Out of line, one copy for all roles: they run once per item, and the
@@ -178,8 +207,10 @@ __device__ __noinline__ float2 item_power(const tc::Params& p, int c1, int c2, i
     return f;
 }
 
-// kRev: chunks visited last to first (the backward's reverse passes).
-template <int KD, bool kRev>
+// kRev: chunks visited last to first (the backward's reverse passes).  kLean:
+// dense, with outputs; the other instance adds packed batches and the states
+// alone (kept in one instance they took 12 % of the dense passes).
+template <int KD, bool kRev, bool kLean>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
@@ -192,7 +223,6 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     uint64_t* k_full = bars + BAR_K_FULL;
     uint64_t* k_empty = bars + BAR_K_EMPTY;
     uint64_t* v_full = bars + BAR_V_FULL;
-    uint64_t* v_read = bars + BAR_V_READ;
     uint64_t* v_empty = bars + BAR_V_EMPTY;
     uint64_t* vt_full = bars + BAR_VT_FULL;
     uint64_t* vt_empty = bars + BAR_VT_EMPTY;
@@ -206,13 +236,22 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     uint64_t* tab_full = bars + BAR_TAB;
     uint64_t* drain = bars + BAR_DRAIN;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + BAR_COUNT);
-    volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    // a wait that runs out ends its role; the others, which then wait for what
+    // it would have done, end the same way
+    bool late = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_bounded(bar, parity);
+        late |= !ok;
+        return ok;
+    };
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int G = gridDim.x;
     const int cta = blockIdx.x;
-    const bool state_only = p.state_only;
+    const bool state_only = !kLean && p.state_only;
+    const bool packed = !kLean && p.mode == 1;
     constexpr bool rev = kRev;
     constexpr int NP = KD / 64;  // 64-column panels per Q / K tile
 
@@ -223,10 +262,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             mbar_init(&k_full[i], 1);
             mbar_init(&k_empty[i], state_only ? 1 : 2);
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_read[i], 8);
-            mbar_init(&v_empty[i], state_only ? 8 : 4);
-            mbar_init(&vt_full[i], 4);
-            mbar_init(&vt_empty[i], 1);
+            mbar_init(&v_empty[i], state_only ? 8 : 9);
             mbar_init(&p_full[i], 1);
             mbar_init(&p_ready[i], 4);
         }
@@ -236,8 +272,11 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         mbar_init(ds_empty, 4);
         mbar_init(s_full, 4);
         mbar_init(tab_full, 4);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&vt_full[i], 4);
+            mbar_init(&vt_empty[i], 1);
+        }
         for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
-        *abort = 0;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -268,23 +307,23 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 const int nc = (it.len + C - 1) / C;
                 for (int c = 0; c < nc; ++c, ++g) {
                     const int t = it.t0 + tc::chunk_row(rev, c, nc);
-                    const int y = p.mode == 0 ? t : it.c1, z = p.mode == 0 ? it.c2 : t;
+                    const int y = !packed ? t : it.c1, z = !packed ? it.c2 : t;
                     const int s = g & 1, n = g >> 1;
-                    if (n > 0 && !mbar_wait(&k_empty[s], (n - 1) & 1, abort, p.status)) { stop = true; break; }
+                    if (n > 0 && !wait(&k_empty[s], (n - 1) & 1)) { stop = true; break; }
                     mbar_arrive_expect_tx(&k_full[s], NP * PANEL);
 #pragma unroll
                     for (int pn = 0; pn < NP; ++pn)
                         tma_load_3d(sm + OFF_K + s * TILE + pn * PANEL, &map_k, &k_full[s], 64 * pn, y, z);
                     ++kg;
                     if (!state_only) {
-                        if (n > 0 && !mbar_wait(&q_empty[s], (n - 1) & 1, abort, p.status)) { stop = true; break; }
+                        if (n > 0 && !wait(&q_empty[s], (n - 1) & 1)) { stop = true; break; }
                         mbar_arrive_expect_tx(&q_full[s], NP * PANEL);
 #pragma unroll
                         for (int pn = 0; pn < NP; ++pn)
                             tma_load_3d(sm + OFF_Q + s * TILE + pn * PANEL, &map_q, &q_full[s], 64 * pn, y, z);
                         ++qg;
                     }
-                    if (n > 0 && !mbar_wait(&v_empty[s], (n - 1) & 1, abort, p.status)) { stop = true; break; }
+                    if (n > 0 && !wait(&v_empty[s], (n - 1) & 1)) { stop = true; break; }
                     mbar_arrive_expect_tx(&v_full[s], PANEL);
                     tma_load_3d(sm + OFF_V + s * PANEL, &map_v, &v_full[s], DVS * it.vs, y, z);
                 }
@@ -310,9 +349,9 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 for (int g = 0; g < total; ++g) {
                     // once O of chunk g-2 has been read out of the buffer
                     const int s = g & 1;
-                    if (g > 1 && !mbar_wait(o_empty, g & 1, abort, p.status)) break;
-                    if (!mbar_wait(&q_full[s], (g >> 1) & 1, abort, p.status)) break;
-                    if (!mbar_wait(&k_full[s], (g >> 1) & 1, abort, p.status)) break;
+                    if (g > 1 && !wait(o_empty, g & 1)) break;
+                    if (!wait(&q_full[s], (g >> 1) & 1)) break;
+                    if (!wait(&k_full[s], (g >> 1) & 1)) break;
                     tc_fence_after();
                     const uint64_t da = tc::kmaj_desc(sq + s * TILE, 0, PANEL), db = tc::kmaj_desc(sk + s * TILE, 0, PANEL);
 #pragma unroll
@@ -324,22 +363,23 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 }
             } else if (warp == WARP_MMA_B) {
                 constexpr uint32_t id_ds = idesc_bf16(128, TERMS * DVS, 1, 1);  // K^T [V1 | V2 | V3]
-                const uint64_t dv = tc::mnmaj_desc(smem_u32(sm + OFF_VT), 0, PANEL);
+                const uint64_t dv = tc::mnmaj_desc(smem_u32(sm + OFF_VT), 0, VT_PANEL);
                 for (int g = 0; g < total; ++g) {
                     const int s = g & 1;
-                    bool ok = mbar_wait(&k_full[s], (g >> 1) & 1, abort, p.status);
-                    ok = ok && (g == 0 || mbar_wait(ds_empty, (g - 1) & 1, abort, p.status));
+                    bool ok = wait(&k_full[s], (g >> 1) & 1);
+                    ok = ok && (g == 0 || wait(ds_empty, (g - 1) & 1));
                     // at d = 64 both 64-row halves of K^T read the same panel (rows 64 .. 127 are ignored)
                     const uint64_t dk = tc::mnmaj_desc(sk + s * TILE, 0, KD == 128 ? PANEL : 0);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && mbar_wait(&vt_full[h], g & 1, abort, p.status);
+                    for (int qd = 0; qd < 4; ++qd) {
+                        ok = ok && wait(&vt_full[qd], g & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
-                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                            mma_ss(tbase + TM_DS, dk + tc::mnmaj_step(kk), dv + tc::mnmaj_step(kk), id_ds, kk > 0);
-                        mma_commit(&vt_empty[h]);
+                        for (int kk = 0; kk < 2; ++kk)
+                            mma_ss(tbase + TM_DS, dk + tc::mnmaj_step(2 * qd + kk), dv + (qd & 1) * (VT_BUF >> 4) + tc::mnmaj_step(kk),
+                                   id_ds, qd + kk > 0);
+                        mma_commit(&vt_empty[qd]);
                     }
                     if (!ok) break;
                     mma_commit(ds_full);
@@ -351,16 +391,17 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 const uint64_t ds = tc::mnmaj_desc(smem_u32(sm + OFF_S), 0, PANEL);
                 for (int g = 0; g < total; ++g) {
                     const int s = g & 1;
-                    if (!mbar_wait(&p_ready[s], (g >> 1) & 1, abort, p.status)) break;
+                    if (!wait(&p_ready[s], (g >> 1) & 1)) break;
                     tc_fence_after();
                     const uint64_t dv = tc::mnmaj_desc(sv + s * PANEL, 0, PANEL);
                     const uint32_t tp = tbase + TM_P + 128u * s;
 #pragma unroll
                     for (int kk = 0; kk < C / 16; ++kk)
                         mma_ts(tp + TM_OPV, tp + kk * 8, dv + tc::mnmaj_step(kk), id_pv, kk > 0);
+                    mma_commit(&v_empty[s]);
                     // (Q has landed: Q K^T has read it)
-                    if (g > 0 && !mbar_wait(o_empty, (g - 1) & 1, abort, p.status)) break;
-                    if (!mbar_wait(s_full, g & 1, abort, p.status)) break;
+                    if (g > 0 && !wait(o_empty, (g - 1) & 1)) break;
+                    if (!wait(s_full, g & 1)) break;
                     tc_fence_after();
                     const uint64_t da = tc::kmaj_desc(sq + s * TILE, 0, PANEL);
 #pragma unroll
@@ -400,35 +441,39 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (t == 0) tab[0] = 1.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(tab_full);
-            if (!tc::warp_wait(tab_full, r & 1, abort, p.status)) break;
+            if (!warp_wait(tab_full, r & 1)) break;
             const int nc = (it.len + C - 1) / C;
             for (int c = 0; c < nc; ++c, ++g) {
                 const int rows = min(C, it.len - tc::chunk_row(rev, c, nc));
                 const int s = g & 1;
-                const bool tail = p.mode == 1 && rows < C;
+                const bool tail = packed && rows < C;
                 const uint32_t v = smem_u32(sm + OFF_V + s * PANEL);
-                if (!tc::warp_wait(&v_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
+                if (!warp_wait(&v_full[s], (g >> 1) & 1)) { stop = true; break; }
                 if (tail) {
                     // rows past the end of a packed sequence hold another one's tokens,
                     // or anything: cleared in V and K, since 0 x NaN is not 0 (Q K^T may
                     // read them either way: those columns of P are masked)
-                    if (!tc::warp_wait(&k_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
+                    if (!warp_wait(&k_full[s], (g >> 1) & 1)) { stop = true; break; }
                     clear_rows(v, rows, t);
 #pragma unroll 1
                     for (int pn = 0; pn < NP; ++pn) clear_rows(smem_u32(sm + OFF_K + s * TILE + pn * PANEL), rows, t);
                 }
-                // --- V terms of the first half of the rows
+                // --- V terms of the first half of the rows, each quarter into the buffer of the one two before it
                 if (!rev && rows < C) w.set<rev>(power, lam16, r0, rows);
-                if (g > 0 && !tc::warp_wait(&vt_empty[0], (g - 1) & 1, abort, p.status)) { stop = true; break; }
-                v_terms(v + static_cast<uint32_t>(t) * 16u, smem_u32(sm + OFF_VT) + static_cast<uint32_t>(t) * 16u, w, r0, rows, tail);
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&vt_full[0]);
-                    mbar_arrive(state_only ? &v_empty[s] : &v_read[s]);
+#pragma unroll 1
+                for (int h = 0; h < 2 && !stop; ++h) {
+                    if (g > 0 && !warp_wait(&vt_empty[2 + h], (g - 1) & 1)) stop = true;
+                    if (stop) break;
+                    v_terms(v + static_cast<uint32_t>(t) * 16u, smem_u32(sm + OFF_VT + h * VT_BUF) + static_cast<uint32_t>(t) * 16u, w, h,
+                            r0, rows, tail);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&vt_full[h]);
                 }
+                if (stop) break;
+                if (lane == 0) mbar_arrive(&v_empty[s]);
                 if (state_only) continue;
                 const uint32_t tp = tlane + TM_P + 128u * s;
-                if (!tc::warp_wait(&p_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
+                if (!warp_wait(&p_full[s], (g >> 1) & 1)) { stop = true; break; }
                 tc_fence_after();
                 // 32-column pieces on the kept side of the diagonal piece take
                 // lam^|l-m| as (factor of the row) x (factor of the column), both
@@ -523,18 +568,21 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 const int s = g & 1;
                 // --- V terms of the second half of the rows
                 if (!rev && rows < C) w.set<rev>(power, lam16, r0, rows);
-                if (!tc::warp_wait(&v_full[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
-                if (g > 0 && !tc::warp_wait(&vt_empty[1], (g - 1) & 1, abort, p.status)) { stop = true; break; }
-                v_terms(smem_u32(sm + OFF_V + s * PANEL) + static_cast<uint32_t>(512 + t) * 16u,
-                        smem_u32(sm + OFF_VT) + static_cast<uint32_t>(512 + t) * 16u, w, r0, rows, p.mode == 1 && rows < C);
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&vt_full[1]);
-                    mbar_arrive(state_only ? &v_empty[s] : &v_read[s]);
+                if (!warp_wait(&v_full[s], (g >> 1) & 1)) { stop = true; break; }
+#pragma unroll 1
+                for (int h = 0; h < 2 && !stop; ++h) {
+                    if (!warp_wait(&vt_empty[h], g & 1)) stop = true;
+                    if (stop) break;
+                    v_terms(smem_u32(sm + OFF_V + s * PANEL) + static_cast<uint32_t>(512 + t) * 16u,
+                            smem_u32(sm + OFF_VT + h * VT_BUF) + static_cast<uint32_t>(t) * 16u, w, h, r0, rows, packed && rows < C);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&vt_full[2 + h]);
                 }
+                if (stop) break;
+                if (lane == 0) mbar_arrive(&v_empty[s]);
                 if (!state_only) {
                     // publish bf16(S) once Q S of the chunk before has read the old one
-                    if (g > 0 && !tc::warp_wait(o_full, (g - 1) & 1, abort, p.status)) { stop = true; break; }
+                    if (g > 0 && !warp_wait(o_full, (g - 1) & 1)) { stop = true; break; }
                     if (own) {
 #pragma unroll
                         for (int ch = 0; ch < 8; ++ch)
@@ -547,7 +595,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 }
                 if (c == odd_at) lam = power(odd);
                 const uint64_t fh = f32x2(lam.x, lam.x), fl = f32x2(lam.y, lam.y);
-                if (!tc::warp_wait(ds_full, g & 1, abort, p.status)) { stop = true; break; }
+                if (!warp_wait(ds_full, g & 1)) { stop = true; break; }
                 tc_fence_after();
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -586,38 +634,33 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const int row = q4 * 32 + lane;
         const uint32_t tlane = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
         int g = 0;
-        int pending = -1;  // V slot whose O store may still be reading it
         bool stop = state_only;
         for (int r = 0; !stop; ++r) {
             const int idx = tc::item_index(r, cta, G);
             if (idx >= p.n_items) break;
             const tc::Item it = item<KD>(p, idx);
             const int nc = (it.len + C - 1) / C;
-            const float g2 = p.log_decay[p.mode == 0 ? it.c2 % p.H : it.c1] * 1.4426950408889634f;
+            const float g2 = p.log_decay[!packed ? it.c2 % p.H : it.c1] * 1.4426950408889634f;
             for (int c = 0; c < nc; ++c, ++g) {
                 const int c0 = tc::chunk_row(rev, c, nc);
                 const int rows = min(C, it.len - c0);
                 const int s = g & 1;
-                // the chunk before has been stored from its V slot
-                if (lane == 0 && pending >= 0) {
-                    bulk_wait_read<0>();
-                    mbar_arrive(&v_empty[pending]);
-                }
+                // the chunk before has been stored from the staging rows
+                if (lane == 0) bulk_wait_read<0>();
                 __syncwarp();
                 // lam^n of this row (rounded to bf16 with the output: a plain fp32
                 // power will do)
                 const int n = rev ? max(rows - 1 - row, 0) : row + 1;
                 const float fac = n == 0 ? 1.f : exp2f(static_cast<float>(n) * g2);
                 const uint64_t f2 = f32x2(fac, fac);
-                // where the row goes: through the chunk's V slot with TMA (a dense
+                // where the row goes: through staging rows with TMA (a dense
                 // tensor clips rows past N itself), row by row on the ragged tail of
                 // a packed sequence, whose next rows belong to another one, or nowhere
-                const int how = q4 * 32 >= rows ? 0 : (p.mode == 0 || q4 * 32 + 32 <= rows) ? 1 : row < rows ? 2 : 0;
-                uint8_t* stg = sm + OFF_V + s * PANEL + q4 * 4096;
+                const int how = q4 * 32 >= rows ? 0 : (!packed || q4 * 32 + 32 <= rows) ? 1 : row < rows ? 2 : 0;
+                uint8_t* stg = sm + OFF_OST + q4 * 4096;
                 const uint32_t sa = smem_u32(stg) + static_cast<uint32_t>(lane) * 128u;
                 uint4* dst = reinterpret_cast<uint4*>(p.o + ((long)(it.t0 + c0 + row) * p.H + it.c1) * p.dv + DVS * it.vs);
-                if (!tc::warp_wait(&v_read[s], (g >> 1) & 1, abort, p.status)) { stop = true; break; }
-                if (!tc::warp_wait(o_full, g & 1, abort, p.status)) { stop = true; break; }
+                if (!warp_wait(o_full, g & 1)) { stop = true; break; }
                 tc_fence_after();
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -648,18 +691,18 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (p.mode == 0) tma_store_3d(&map_o, stg, DVS * it.vs, it.t0 + c0 + q4 * 32, it.c2);
+                        if (!packed) tma_store_3d(&map_o, stg, DVS * it.vs, it.t0 + c0 + q4 * 32, it.c2);
                         else tma_store_3d(&map_o, stg, DVS * it.vs, it.c1, it.t0 + c0 + q4 * 32);
                         bulk_commit();
                     }
                 }
-                pending = s;
             }
         }
         if (lane == 0) bulk_wait<0>();
         __syncwarp();
     }
 
+    if (late) atomicExch(p.status, kStatusTimeout);
     tc_fence_before();
     __syncthreads();
     if (warp == WARP_MMA_A) {
