@@ -4,7 +4,8 @@
  * The operation (page "MiniMax-M1で理解する：大規模言語モデルのコンテキスト長
  * 限界を突破する革新的アーキテクチャ" (zenn.dev), section "線形アテンションの
  * 数学的基礎"), with the feature map phi = identity, no decay, no normaliser and
- * no 1/sqrt(d) scale (the pages fix none of them):
+ * no 1/sqrt(d) scale (the pages fix none of them; the calls with a decay per
+ * head are further below):
  *
  *     S_t = S_{t-1} + k_t (x) v_t        (outer product; S is d_k x d_v, fp32)
  *     o_t = q_t S_t                      (q_t a row vector; inclusive of token t)
@@ -29,7 +30,7 @@
  *    as la_status, launch errors as LA_ERR_CUDA (see la_last_error()).
  *  - Alignment: every tensor pointer must be 16-byte aligned.
  *  - Aliasing: no input may alias an output, except the in-place state of
- *    la_decode_step.
+ *    the decode step calls.
  *  - Dimensions: d_k = d_v = d with d in {64, 128}.  bf16 inputs run on the
  *    tcgen05 tensor-core path; fp32 inputs run on a CUDA-core FFMA path.
  *    Anything else returns LA_ERR_UNSUPPORTED.
