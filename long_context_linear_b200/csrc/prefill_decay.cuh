@@ -298,7 +298,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
             int g = 0;      // chunks whose copies are all issued
-            int kg = 0, qg = 0;  // copies of K and Q issued
+            int kg = 0, vg = 0, qg = 0;  // copies of K, V and Q issued
             bool stop = false;
             for (int r = 0; !stop; ++r) {
                 const int idx = tc::item_index(r, cta, G);
@@ -315,6 +315,11 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     for (int pn = 0; pn < NP; ++pn)
                         tma_load_3d(sm + OFF_K + s * TILE + pn * PANEL, &map_k, &k_full[s], 64 * pn, y, z);
                     ++kg;
+                    if (n > 0 && !wait(&v_empty[s], (n - 1) & 1)) { stop = true; break; }
+                    mbar_arrive_expect_tx(&v_full[s], PANEL);
+                    tma_load_3d(sm + OFF_V + s * PANEL, &map_v, &v_full[s], DVS * it.vs, y, z);
+                    ++vg;
+                    // (Q last: its slot is the one held longest)
                     if (!state_only) {
                         if (n > 0 && !wait(&q_empty[s], (n - 1) & 1)) { stop = true; break; }
                         mbar_arrive_expect_tx(&q_full[s], NP * PANEL);
@@ -323,15 +328,12 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                             tma_load_3d(sm + OFF_Q + s * TILE + pn * PANEL, &map_q, &q_full[s], 64 * pn, y, z);
                         ++qg;
                     }
-                    if (n > 0 && !wait(&v_empty[s], (n - 1) & 1)) { stop = true; break; }
-                    mbar_arrive_expect_tx(&v_full[s], PANEL);
-                    tma_load_3d(sm + OFF_V + s * PANEL, &map_v, &v_full[s], DVS * it.vs, y, z);
                 }
             }
             // no copy into shared memory may still be in flight at exit
             for (int x = max(kg - 2, 0); x < kg; ++x) tc::drain_wait(&k_full[x & 1], (x >> 1) & 1);
             for (int x = max(qg - 2, 0); x < qg; ++x) tc::drain_wait(&q_full[x & 1], (x >> 1) & 1);
-            for (int x = max(g - 2, 0); x < g; ++x) tc::drain_wait(&v_full[x & 1], (x >> 1) & 1);
+            for (int x = max(vg - 2, 0); x < vg; ++x) tc::drain_wait(&v_full[x & 1], (x >> 1) & 1);
         }
     } else if (warp == WARP_MMA_A || warp == WARP_MMA_B || warp == WARP_MMA_C) {
         // ------------------------------------------------------ MMA threads
