@@ -306,6 +306,11 @@ LA_API la_status la_prefill_backward_ex(const void* q, const void* k, const void
  *   G_N = q_N^T dout_N + ds_n,  G_t = q_t^T dout_t + exp(g) G_{t+1},
  *   dq_t = dout_t S_t^T,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  ds0 = exp(g) G_1
  * (N = 0: ds0 = ds_n).
+ *
+ * The workspaces are optional, as there, and their sizes are these calls' own:
+ * with them, bf16 batches of more (head, 64 value columns) items than SMs are
+ * shared out by chunks of 128 tokens instead of whole sequences (the same bits,
+ * in less time).  One workspace serves one call at a time.
  */
 LA_API size_t la_prefill_decay_workspace_size(int B, int H, int N, int dk, int dv, la_dtype dt);
 LA_API la_status la_prefill_decay(const void* q, const void* k, const void* v, void* o, const float* s0, float* s_out,

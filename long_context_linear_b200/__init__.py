@@ -139,7 +139,8 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional[torc
         _check_decay(log_decay, H, q.device, phi)
         if tuple(out.shape) != (B, H, N, dv) or (s_out is not None and tuple(s_out.shape) != (B, H, dk, dv)):
             raise ValueError("out must be [B, H, N, dv] and s_out [B, H, dk, dv]")
-    need = int(lib.la_prefill_workspace_size_ex(B, H, N, dk, dv, dt, _phi_code(phi)))
+    need = int(lib.la_prefill_workspace_size_ex(B, H, N, dk, dv, dt, _phi_code(phi)) if log_decay is None
+               else lib.la_prefill_decay_workspace_size(B, H, N, dk, dv, dt))
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -223,7 +224,8 @@ def prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: to
         _check_decay(log_decay, H, q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds0 = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if need_ds0 else None
-    need = int(lib.la_prefill_backward_workspace_size(B, H, N, d, d, _dtype_code(q)))
+    need = int((lib.la_prefill_backward_workspace_size if log_decay is None
+                else lib.la_prefill_decay_backward_workspace_size)(B, H, N, d, d, _dtype_code(q)))
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()

@@ -23,7 +23,8 @@
 //
 // Work item = (unit or sequence and head, 64 value columns), persistent CTAs,
 // as in prefill_tc.cuh, whose items, segments, reverse order and packed batches
-// it shares.  In reverse order rows take lam^(m-l) and lam^(R-1-l), the update
+// it shares; dense items that are not a multiple of the SMs are shared out by
+// chunks (piece()).  In reverse order rows take lam^(m-l) and lam^(R-1-l), the update
 // lam^(m+1) (the state is held already decayed).
 //
 // Shared memory (217 KB): Q 2 x 32 KB, K 2 x 32 KB, V 2 x 16 KB, the three V
@@ -152,7 +153,7 @@ struct Weights {
     }
 };
 // Quarter h (0, 1) of the group's 64 rows, whose places in V start at v.
-// (rolled: see item())
+// (rolled: see piece())
 __device__ __forceinline__ void v_terms(uint32_t v, uint32_t vt, const Weights& w, int h, int r0, int rows, bool tail) {
     float wa = h ? w.w[2] : w.w[0];
     const float wb = h ? w.w[3] : w.w[1];
@@ -177,7 +178,7 @@ __device__ __noinline__ void clear_rows(uint32_t tile, int rows, int t) {
 }
 
 // Bounded wait for the phase of the given parity, in few instructions (see
-// item()): up to 100,000 tries, each of which sleeps for up to 20 us or until
+// piece()): up to 100,000 tries, each of which sleeps for up to 20 us or until
 // the phase completes; two seconds in all at most.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -196,9 +197,79 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
 // kernel's instruction footprint is what its loops wait for (all roles of all
 // SMs run at once; with these inlined and everything unrolled it was 112 KB and
 // took 10,000 cycles per chunk).
-template <int KD>
-__device__ __noinline__ tc::Item item(const tc::Params& p, int idx) {
-    return tc::decode_item<true, KD>(p, idx);
+//
+// What CTA `cta` of `G` does in turn r: an item, or part of one; len < 0 when
+// it has no more.  With more items than CTAs whole items in turn leave CTAs idle
+// in the last turn (150 items take twice as long as 148).  The wrapped schedule
+// instead lays the chunks of all units of a value slice end to end and cuts the
+// row into equal shares, p.wrap chunks each.  A unit that a cut divides is begun
+// by the CTA below the cut, as the first thing it does, and finished by the one
+// above, as the last: with a share no shorter than a unit the state to go on
+// from has long been written (wait_state).  A CTA waits for a lower one's first
+// piece, which waits for nothing, and all are resident (cooperative launch).
+// The two slices of a unit share Q and K: their CTAs, neighbours, keep step.
+struct Piece : tc::Item {
+    const float* init;  // initial state of this value slice, rows init_ld apart, or null
+    float* out;         // where the state goes, or null
+    int init_ld, out_ld;
+    int from, to;       // CTA whose state is continued, own slot written for the next one (or -1)
+};
+template <int KD, bool kRev, bool kLean>
+__device__ __noinline__ Piece piece(const tc::Params& p, int r, int cta, int G) {
+    constexpr int NV = KD / DVS;
+    constexpr long SLOT = (long)KD * DVS;
+    Piece it;
+    it.from = it.to = -1;
+    int idx = tc::item_index(r, cta, G), from = 0, to = 0;
+    const int n = (p.N + C - 1) / C;
+    const bool wrapped = kLean && p.wrap > 0;
+    if (wrapped) {
+        const long lo = (long)(cta / NV) * p.wrap, hi = min(lo + p.wrap, (long)(p.n_items / NV) * n);
+        const long u = (hi - 1) / n - r;
+        if (hi <= lo || (u + 1) * n <= lo) idx = p.n_items;
+        else {
+            idx = (int)u * NV + cta % NV;
+            from = (int)(max(lo, u * n) - u * n);
+            to = (int)(min(hi, (u + 1) * n) - u * n);
+        }
+    }
+    if (idx >= p.n_items) {
+        it.len = -1;
+        return it;
+    }
+    static_cast<tc::Item&>(it) = tc::decode_item<true, KD>(p, idx);
+    it.init = static_cast<const tc::Item&>(it).init;
+    if (it.init) it.init += p.init_transposed ? (long)DVS * it.vs * KD : DVS * it.vs;
+    it.init_ld = p.dv;
+    it.out = p.s_out && it.write_state ? p.s_out + it.state * KD * p.dv + DVS * it.vs : nullptr;
+    it.out_ld = p.dv;
+    if (wrapped) {
+        // chunks [from, to) in visiting order
+        it.t0 = (kRev ? n - to : from) * C;
+        it.len = min(p.N, (kRev ? n - from : to) * C) - it.t0;
+        if (from > 0) {
+            it.from = cta - NV;
+            it.init = p.wrap_state + it.from * SLOT;
+            it.init_ld = DVS;
+        }
+        if (to < n) {
+            it.to = cta;
+            it.out = p.wrap_state + cta * SLOT;
+            it.out_ld = DVS;
+        }
+    }
+    return it;
+}
+// Waits until the state warps of another CTA have all written their rows of its
+// slot; a second at most.
+__device__ __noinline__ bool wait_state(const int* ready) {
+    for (int i = 0; i < 500000; ++i) {
+        int n;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(n) : "l"(ready) : "memory");
+        if (n >= 4) return true;
+        __nanosleep(1000);
+    }
+    return false;
 }
 // lam^n as two fp32 values, for the head of `it`
 __device__ __noinline__ float2 item_power(const tc::Params& p, int c1, int c2, int n) {
@@ -301,9 +372,8 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             int kg = 0, vg = 0, qg = 0;  // copies of K, V and Q issued
             bool stop = false;
             for (int r = 0; !stop; ++r) {
-                const int idx = tc::item_index(r, cta, G);
-                if (idx >= p.n_items) break;
-                const tc::Item it = item<KD>(p, idx);
+                const Piece it = piece<KD, kRev, kLean>(p, r, cta, G);
+                if (it.len < 0) break;
                 const int nc = (it.len + C - 1) / C;
                 for (int c = 0; c < nc; ++c, ++g) {
                     const int t = it.t0 + tc::chunk_row(rev, c, nc);
@@ -341,9 +411,9 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             const uint32_t sq = smem_u32(sm + OFF_Q), sk = smem_u32(sm + OFF_K), sv = smem_u32(sm + OFF_V);
             int total = 0;  // this CTA's chunks
             for (int r = 0;; ++r) {
-                const int idx = tc::item_index(r, cta, G);
-                if (idx >= p.n_items) break;
-                total += (item<KD>(p, idx).len + C - 1) / C;
+                const int len = piece<KD, kRev, kLean>(p, r, cta, G).len;
+                if (len < 0) break;
+                total += (len + C - 1) / C;
             }
             uint64_t* done = &drain[warp == WARP_MMA_A ? 0 : warp - WARP_MMA_B + 1];
             if (warp == WARP_MMA_A) {
@@ -428,9 +498,8 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         int g = 0;
         bool stop = false;
         for (int r = 0; !stop; ++r) {
-            const int idx = tc::item_index(r, cta, G);
-            if (idx >= p.n_items) break;
-            const tc::Item it = item<KD>(p, idx);
+            const Piece it = piece<KD, kRev, kLean>(p, r, cta, G);
+            if (it.len < 0) break;
             auto power = [&](int n) { return item_power(p, it.c1, it.c2, n); };
             const float2 step = power(16);
             const double lam16 = static_cast<double>(step.x) + step.y;
@@ -535,16 +604,20 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         int g = 0;
         bool stop = false;
         for (int r = 0; !stop; ++r) {
-            const int idx = tc::item_index(r, cta, G);
-            if (idx >= p.n_items) break;
-            const tc::Item it = item<KD>(p, idx);
+            const Piece it = piece<KD, kRev, kLean>(p, r, cta, G);
+            if (it.len < 0) break;
             uint64_t S[DVS / 2];  // pairs of value columns
-            if (it.init && p.init_transposed && own) {
-                const float* src = it.init + (long)DVS * it.vs * KD + i;
+            if (kLean && it.from >= 0) {
+                const bool ok = wait_state(p.wrap_ready + it.from);
+                late |= !ok;
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
+            if (it.init && p.init_transposed && it.from < 0 && own) {
+                const float* src = it.init + i;
 #pragma unroll
                 for (int j = 0; j < DVS; j += 2) S[j / 2] = f32x2(src[j * KD], src[(j + 1) * KD]);
             } else if (it.init && own) {
-                const float4* src = reinterpret_cast<const float4*>(it.init + (long)i * p.dv + DVS * it.vs);
+                const float4* src = reinterpret_cast<const float4*>(it.init + (long)i * it.init_ld);
 #pragma unroll
                 for (int j = 0; j < DVS / 4; ++j) {
                     const float4 x = src[j];
@@ -619,8 +692,8 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 if (rev && c == odd_at) lam = power(C);
             }
             if (stop) break;
-            if (p.s_out && it.write_state && own) {
-                float4* dst = reinterpret_cast<float4*>(p.s_out + (it.state * KD + i) * p.dv + DVS * it.vs);
+            if (it.out && own) {
+                float4* dst = reinterpret_cast<float4*>(it.out + (long)i * it.out_ld);
 #pragma unroll
                 for (int j = 0; j < DVS / 4; ++j) {
                     float4 x;
@@ -628,6 +701,11 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     f32x2_split(S[2 * j + 1], x.z, x.w);
                     dst[j] = x;
                 }
+            }
+            if (kLean && it.to >= 0) {
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.wrap_ready + it.to) : "memory");
             }
         }
     } else {
@@ -638,9 +716,8 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         int g = 0;
         bool stop = state_only;
         for (int r = 0; !stop; ++r) {
-            const int idx = tc::item_index(r, cta, G);
-            if (idx >= p.n_items) break;
-            const tc::Item it = item<KD>(p, idx);
+            const Piece it = piece<KD, kRev, kLean>(p, r, cta, G);
+            if (it.len < 0) break;
             const int nc = (it.len + C - 1) / C;
             const float g2 = p.log_decay[!packed ? it.c2 % p.H : it.c1] * 1.4426950408889634f;
             for (int c = 0; c < nc; ++c, ++g) {

@@ -349,3 +349,74 @@ def test_wrapper_refusals(la):
         la.prefill(x, x, x, log_decay=g, phi="relu")
     with pytest.raises(ValueError):
         la.prefill(x, x, x, log_decay=g, out=torch.empty(1, 2, 4, 64, dtype=torch.bfloat16, device="cuda"))
+
+
+# sizes whose (unit, 64 value columns) items leave SMs idle in the last turn: a
+# unit's chunks are then divided between two CTAs, which hand its state on
+SHARED = [(128, 1, 76, 700), (128, 5, 15, 1025), (128, 3, 50, 640), (64, 1, 149, 900), (64, 10, 20, 1300)]
+
+
+@pytest.mark.parametrize("d,B,H,N", SHARED)
+@pytest.mark.parametrize("resume", [False, True])
+def test_prefill_shared_out_by_chunks(la, d, B, H, N, resume):
+    q, k, v = synth.dense(B, H, N, d, "bf16", seed=23)
+    g = ladder(H, "mix")
+    s0 = states(B, H, d, 24) if resume else None
+    assert la.lib.la_prefill_decay_workspace_size(B, H, N, d, d, la._abi.LA_BF16) > 0
+    o, s = run_prefill(la, q, k, v, g, s0)
+    # without the workspace whole items run in turn: the same arithmetic
+    c = cuda(q, k, v, s0, g)
+    o1, s1 = torch.empty_like(c[0]), torch.empty(B, H, d, d, device="cuda")
+    ptr = [None if t is None else t.data_ptr() for t in c]
+    st = torch.cuda.current_stream().cuda_stream
+    assert la.lib.la_prefill_decay(ptr[0], ptr[1], ptr[2], o1.data_ptr(), ptr[3], s1.data_ptr(), ptr[4], B, H, N, d, d,
+                                   la._abi.LA_BF16, 0, None, 0, st) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(o, o1.cpu()) and torch.equal(s, s1.cpu())
+    ro, rs = od.recurrent(q, k, v, g, s0)
+    assert_out(o, ro, q.dtype, 2)
+    assert_state(s, rs, 2, tol=STATE)
+
+
+@pytest.mark.parametrize("d,B,H,N", SHARED[1:4])
+def test_backward_shared_out_by_chunks(la, d, B, H, N):
+    q, k, v = synth.dense(B, H, N, d, "bf16", seed=25)
+    do = synth.dense(B, H, N, d, "bf16", seed=26)[2]
+    g, s0, ds = ladder(H, "mix"), states(B, H, d, 27), states(B, H, d, 28)
+    c = cuda(q, k, v, do, s0, ds, g)
+    got = la.prefill_backward(*c[:6], log_decay=c[6])
+    want = [torch.empty_like(t) for t in got]
+    assert la.lib.la_prefill_decay_backward(*(t.data_ptr() for t in c), *(t.data_ptr() for t in want), B, H, N, d, d,
+                                            la._abi.LA_BF16, None, 0, torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert la.device_status() == 0
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
+def test_shared_out_captured_and_on_two_streams(la):
+    B, H, N, d = 3, 50, 640, 128
+    q, k, v = (t.cuda() for t in synth.dense(B, H, N, d, "bf16", seed=29))
+    g = ladder(H).cuda()
+    want = la.prefill(q, k, v, log_decay=g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        la.prefill(q, k, v, log_decay=g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, s = la.prefill(q, k, v, log_decay=g)
+    for _ in range(3):
+        o.zero_()
+        s.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            o2, s2 = la.prefill(q, k, v, log_decay=g)
+        torch.cuda.synchronize()
+        for a, b in zip(want, (o, s)):
+            assert torch.equal(a, b)
+        for a, b in zip(want, (o2, s2)):
+            assert torch.equal(a, b)
+    assert la.device_status() == 0
