@@ -77,6 +77,8 @@ std::mutex g_dev_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
+constexpr int kSimtDefaultChunk = 64;
+
 template <typename T, bool kDecay>
 cudaError_t set_simt_attrs() {
     cudaError_t e;
@@ -164,6 +166,13 @@ la_status device_info(DeviceInfo** out) {
             (e = set_simt_attrs<__nv_bfloat16, false>()) != cudaSuccess ||
             (e = set_simt_attrs<float, true>()) != cudaSuccess || (e = set_simt_attrs<__nv_bfloat16, true>()) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(prefill_simt)");
+        if ((e = cudaFuncSetAttribute(simt::prefill_simt_batch_kernel<float, 128, kSimtDefaultChunk>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      simt::smem_bytes<128, kSimtDefaultChunk>())) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(simt::prefill_simt_batch_kernel<float, 64, kSimtDefaultChunk>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      simt::smem_bytes<64, kSimtDefaultChunk>())) != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute(prefill_simt_batch)");
         const void* decay_kernels[8] = {reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, true, false>),
                                         reinterpret_cast<const void*>(tcd::prefill_decay_kernel<64, true, false>),
                                         reinterpret_cast<const void*>(tcd::prefill_decay_kernel<128, false, true>),
@@ -256,7 +265,6 @@ la_status check_dims(int dk, int dv, la_dtype dt) {
 
 bool use_tensor_cores(int d, la_dtype dt) { return dt == LA_BF16 && (d == 128 || d == 64); }
 
-constexpr int kSimtDefaultChunk = 64;
 
 la_status check_chunk(int chunk, bool tcpath) {
     if (chunk == 0) return LA_OK;
@@ -684,6 +692,80 @@ la_status simt_dense(const void* q, const void* k, const void* v, void* o, const
     sp.seg_init = starts;
     return go(sp, U * P);
 }
+
+namespace {
+// Segments of a sequence when the three passes of a backward share the SMs.
+int plan_backward_batch(long U, int N, int sms, int* seg_len) {
+    return plan_segments(3 * U, N, 1, sms, seg_len, kSimtDefaultChunk, kMinSegChunksSimt);
+}
+
+// The passes of the decayed fp32 backward (prefill_backward) side by side: three
+// launches, or one without segments.
+la_status simt_backward_batch(const float* q, const float* k, const float* v, const float* dout, const float* s0,
+                              const float* ds_n, float* dq, float* dk, float* dv, float* ds0, const float* log_decay,
+                              int H, long U, int N, int d, DeviceInfo* di, void* ws, size_t ws_bytes, cudaStream_t st) {
+    simt::Batch<float> b{{dout, v, k}, {v, dout, q}, {k, q, dout}, {dq, dk, dv}, {}};
+    const float* init[3] = {s0, ds_n, ds_n};
+    const int rev[3] = {0, 1, 1}, init_t[3] = {1, 1, 0};
+    int seg_len;
+    int P = plan_backward_batch(U, N, di->sms, &seg_len);
+    const size_t one = segment_workspace_bytes(U, P, d, d);
+    if (P > 1 && (!ws || ws_bytes < 3 * one || !aligned16(ws) || U * P > (1L << 30))) P = 1;
+    for (int y = 0; y < 3; ++y) {
+        simt::Params& p = b.p[y];
+        p.N = N;
+        p.s0 = init[y];
+        p.s_out = y == 2 ? ds0 : nullptr;
+        p.phi = LA_PHI_IDENTITY;
+        p.reverse = rev[y];
+        p.init_transposed = init_t[y];
+        p.log_decay = log_decay;
+        p.heads = H;
+    }
+    auto go = [&](const simt::Batch<float>& x, long grid, const char* what) {
+        const dim3 g((unsigned)grid, 3);
+        if (d == 128)
+            simt::prefill_simt_batch_kernel<float, 128, kSimtDefaultChunk>
+                <<<g, simt::NUM_THREADS, simt::smem_bytes<128, kSimtDefaultChunk>(), st>>>(x);
+        else
+            simt::prefill_simt_batch_kernel<float, 64, kSimtDefaultChunk>
+                <<<g, simt::NUM_THREADS, simt::smem_bytes<64, kSimtDefaultChunk>(), st>>>(x);
+        return after_launch(what);
+    };
+    if (P > 1) {
+        simt::Batch<float> sums = b;
+        segp::Batch pre{};
+        for (int y = 0; y < 3; ++y) {
+            float* at = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + y * one);
+            simt::Params& p = sums.p[y];
+            p.n_seg = P - 1;
+            p.seg_len = seg_len;
+            p.seg_base = rev[y];
+            p.s0 = nullptr;
+            p.init_transposed = 0;
+            p.s_out = at;
+            p.s_out_per_seg = 1;
+            p.state_only = 1;
+            pre.sums[y] = at;
+            pre.s0[y] = init[y];
+            pre.starts[y] = at + (size_t)U * (P - 1) * d * d;
+            pre.reverse[y] = rev[y];
+            pre.s0_transposed[y] = init_t[y];
+            b.p[y].n_seg = P;
+            b.p[y].seg_len = seg_len;
+            b.p[y].seg_init = pre.starts[y];
+        }
+        la_status s;
+        if ((s = go(sums, U * (P - 1), "backward segment sums launch")) != LA_OK) return s;
+        const long threads = U * (long)(d * d / 4);
+        const int blocks = (int)std::min<long>((threads + segp::NUM_THREADS - 1) / segp::NUM_THREADS, 2L * di->sms);
+        segp::seg_prefix_batch_kernel<<<dim3(blocks, 3), segp::NUM_THREADS, 0, st>>>(pre, U, P, d, log_decay, H, seg_len,
+                                                                                  N - (P - 1) * seg_len);
+        if ((s = after_launch("backward segment prefix launch")) != LA_OK) return s;
+    }
+    return go(b, U * P, "backward launch");
+}
+}  // namespace
 
 size_t la_prefill_workspace_size(int B, int H, int N, int dk, int dv, la_dtype dt) {
     return la_prefill_workspace_size_ex(B, H, N, dk, dv, dt, LA_PHI_IDENTITY);
@@ -1437,6 +1519,10 @@ static la_status prefill_backward(const void* q, const void* k, const void* v, c
         return tc_dense_pass(k, q, dout, dv, ds_n, false, ds0, true, log_decay, H, U, N, d_k, di, st, workspace, ws_bytes);
     }
     if (N == 0 && !ds0) return LA_OK;
+    if (decayed && dt == LA_FP32 && N > 0)
+        return simt_backward_batch((const float*)q, (const float*)k, (const float*)v, (const float*)dout, s0, ds_n,
+                                   (float*)dq, (float*)dk, (float*)dv, ds0, log_decay, H, U, N, d_k, di, workspace,
+                                   ws_bytes, st);
     if (N > 0) {
         if ((s = simt_dense(dout, v, k, dq, s0, true, nullptr, false, LA_PHI_IDENTITY, log_decay, H, U, N, d_k, dt, 0, di,
                             workspace, ws_bytes, st)) != LA_OK)
@@ -1458,6 +1544,12 @@ la_status la_prefill_backward_ex(const void* q, const void* k, const void* v, co
 }
 
 size_t la_prefill_decay_backward_workspace_size(int B, int H, int N, int d_k, int d_v, la_dtype dt) {
+    DeviceInfo* di;
+    if (dt == LA_FP32 && B > 0 && H > 0 && N > 0 && d_k == d_v && (d_k == 64 || d_k == 128) && device_info(&di) == LA_OK) {
+        int seg_len;
+        const long U = (long)B * H;
+        return 3 * segment_workspace_bytes(U, plan_backward_batch(U, N, di->sms, &seg_len), d_k, d_v);
+    }
     return std::max(la_prefill_backward_workspace_size(B, H, N, d_k, d_v, dt), wrap_size(B, H, N, d_k, d_v, dt));
 }
 

@@ -29,11 +29,11 @@ constexpr int NUM_THREADS = 256;
 // transpose of a d x d state (elems = d * d).  kDecay: log_decay [H], unit u of
 // head u % H; every segment but the last in memory has seg_len tokens, which
 // has tail_len.
-template <bool kDecay = false>
-__global__ void __launch_bounds__(NUM_THREADS)
-seg_prefix_kernel(const float* __restrict__ seg_sums, const float* __restrict__ s0, float* __restrict__ starts,
-                  long U, int n_seg, int elems, int reverse, int s0_transposed, int d,
-                  const float* __restrict__ log_decay = nullptr, int H = 1, int seg_len = 0, int tail_len = 0) {
+template <bool kDecay>
+__device__ __forceinline__ void seg_prefix_body(const float* __restrict__ seg_sums, const float* __restrict__ s0,
+                                                float* __restrict__ starts, long U, int n_seg, int elems, int reverse,
+                                                int s0_transposed, int d, const float* __restrict__ log_decay, int H,
+                                                int seg_len, int tail_len) {
     const int per_unit = elems / 4;
     for (long t = (long)blockIdx.x * blockDim.x + threadIdx.x; t < U * per_unit; t += (long)gridDim.x * blockDim.x) {
         const long u = t / per_unit;
@@ -75,6 +75,30 @@ seg_prefix_kernel(const float* __restrict__ seg_sums, const float* __restrict__ 
             }
         }
     }
+}
+
+template <bool kDecay = false>
+__global__ void __launch_bounds__(NUM_THREADS)
+seg_prefix_kernel(const float* __restrict__ seg_sums, const float* __restrict__ s0, float* __restrict__ starts,
+                  long U, int n_seg, int elems, int reverse, int s0_transposed, int d,
+                  const float* __restrict__ log_decay = nullptr, int H = 1, int seg_len = 0, int tail_len = 0) {
+    seg_prefix_body<kDecay>(seg_sums, s0, starts, U, n_seg, elems, reverse, s0_transposed, d, log_decay, H, seg_len,
+                            tail_len);
+}
+
+// Three decayed passes over the same sequences at once (blockIdx.y).
+struct Batch {
+    const float* sums[3];
+    const float* s0[3];
+    float* starts[3];
+    int reverse[3], s0_transposed[3];
+};
+__global__ void __launch_bounds__(NUM_THREADS)
+seg_prefix_batch_kernel(const __grid_constant__ Batch b, long U, int n_seg, int d, const float* __restrict__ log_decay,
+                        int H, int seg_len, int tail_len) {
+    const int y = blockIdx.y;
+    seg_prefix_body<true>(b.sums[y], b.s0[y], b.starts[y], U, n_seg, d * d, b.reverse[y], b.s0_transposed[y], d, log_decay,
+                          H, seg_len, tail_len);
 }
 
 // The same for a packed batch whose sequences have different segment counts

@@ -420,3 +420,16 @@ def test_shared_out_captured_and_on_two_streams(la):
         for a, b in zip(want, (o2, s2)):
             assert torch.equal(a, b)
     assert la.device_status() == 0
+
+
+@pytest.mark.parametrize("d,B,H,N", [(64, 1, 3, 777), (128, 2, 9, 200)])
+def test_fp32_backward_without_a_workspace(la, d, B, H, N):
+    q, k, v = synth.dense(B, H, N, d, "fp32", seed=61)
+    dout = synth.dense(B, H, N, d, "fp32", seed=62)[2]
+    g, s0, ds = ladder(H, "mix"), states(B, H, d, 63), states(B, H, d, 64)
+    c = cuda(q, k, v, dout, s0, ds, g)
+    got = [torch.empty_like(t) for t in (*c[:3], c[4])]
+    assert la.lib.la_prefill_decay_backward(*(t.data_ptr() for t in c), *(t.data_ptr() for t in got), B, H, N, d, d,
+                                            la._abi.LA_FP32, None, 0, torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    _check_grads(got, od.backward(q, k, v, dout, g, s0, ds), q.dtype)
