@@ -354,7 +354,8 @@ typedef struct {
  *          d in {64, 128}, any strides that keep rows 16-byte aligned: q and k
  *          may be slices of one projection's output, q_out and k_out the
  *          contiguous [B, H, N, d], [T, H, d] (B = 1) or [B, H, d] (N = 1) that
- *          the attention calls read.  Outputs must not overlap inputs.
+ *          the attention calls read.  Outputs must not overlap inputs, nor have a
+ *          stride of 0 in a dimension of more than one entry (inputs may).
  *   q_weight, k_weight: [d] in `dt` or fp32 (`wdt`), 16-byte aligned.
  *   inv_freq: fp32 [rot / 2]; rot: a multiple of 16 in [0, d] (0: norm only).
  *   positions: int32 (pos64 = 0) or int64 (pos64 != 0), token (b, n) at

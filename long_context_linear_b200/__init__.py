@@ -49,7 +49,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device: torch.device):
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle alone, without a stream object around it (2 us of a call's 17)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
 
 
 class _Here:
@@ -144,7 +145,7 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional[torc
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         if log_decay is not None:
             _abi.check(lib.la_prefill_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(s0), _ptr(s_out),
                                             _ptr(log_decay), B, H, N, dk, dv, dt, chunk, _ptr(workspace), ws_bytes,
@@ -229,7 +230,7 @@ def prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: to
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         if log_decay is not None:
             _abi.check(lib.la_prefill_decay_backward(
                 _ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(s0), _ptr(ds_n), _ptr(log_decay), _ptr(dq), _ptr(dk),
@@ -301,7 +302,7 @@ def prefill_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         if log_decay is not None:
             _abi.check(lib.la_prefill_varlen_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(cu_seqlens), n_seq, T,
                                                    _ptr(state_pool), n_pool, _ptr(init_idx), _ptr(s_out),

@@ -293,7 +293,7 @@ la_status after_launch(const char* what) {
 // option needs the general one, which carries the feature-map code only when
 // a feature map is applied in the kernel.
 la_status launch_tc(int grid, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                    const CUtensorMap& mo, const tc::Params& p, cudaStream_t st, const char* what) {
+                    const CUtensorMap& mo, const tcd::Params& p, cudaStream_t st, const char* what) {
     const bool phi = p.phi != LA_PHI_IDENTITY;
     const bool general =
         phi || p.reverse || p.state_only || p.init_transposed || (p.mode == 0 && p.n_seg > 1) || p.seg_off;
@@ -356,7 +356,7 @@ size_t wrap_workspace_bytes(long U, int N, int d, int sms) {
 }
 // Sets up the wrapped schedule for a pass over whole sequences where it gains and
 // the workspace has room, and the grid.
-la_status plan_wrap(tc::Params* p, long U, int d, int sms, void* ws, size_t ws_bytes, cudaStream_t st, int* grid) {
+la_status plan_wrap(tcd::Params* p, long U, int d, int sms, void* ws, size_t ws_bytes, cudaStream_t st, int* grid) {
     const size_t need = p->log_decay ? wrap_workspace_bytes(U, p->N, d, sms) : 0;
     if (!need || !ws || ws_bytes < need || !aligned16(ws)) return LA_OK;
     p->wrap = wrap_chunks(U, p->N, d, sms);
@@ -822,7 +822,7 @@ static la_status prefill_dense(const void* q, const void* k, const void* v, void
                           ws_bytes, st);
 
     const int nvs = tc_slices(dv);
-    tc::Params p{};
+    tcd::Params p{};
     p.mode = 0;
     p.dk = dk;
     p.n_items = (int)(U * nvs);
@@ -875,7 +875,7 @@ static la_status prefill_dense(const void* q, const void* k, const void* v, void
         // (2) the state before every segment, (3) all segments from those states
         float* seg_sums = reinterpret_cast<float*>(workspace);
         float* starts = seg_sums + (size_t)U * (P - 1) * dk * dv;
-        tc::Params p1 = p;
+        tcd::Params p1 = p;
         p1.n_seg = P - 1;
         p1.n_items = (int)(U * (P - 1) * nvs);
         p1.s0 = nullptr;
@@ -1116,7 +1116,7 @@ static la_status prefill_packed(const void* q, const void* k, const void* v, voi
         max_segs = 0;  // no room for the segment states: whole sequences
     const long max_nl = max_segs - n_seq;
 
-    tc::Params p{};
+    tcd::Params p{};
     p.mode = 1;
     p.n_seg = 1;
     p.phi = phi;
@@ -1159,7 +1159,7 @@ static la_status prefill_packed(const void* q, const void* k, const void* v, voi
         p.n_seq = n_seq;
         p.seg_len_dev = seg_len;
         if (max_nl > 0) {
-            tc::Params p1 = p;
+            tcd::Params p1 = p;
             p1.state_only = 1;
             p1.n_items = (int)(max_nl * H * nvs);
             p1.s_out = sums;
@@ -1394,7 +1394,7 @@ static la_status tc_dense_pass(const void* q, const void* k, const void* v, void
                                DeviceInfo* di, cudaStream_t st, void* ws, size_t ws_bytes) {
     if (N == 0 && !s_out) return LA_OK;
     const int nvs = tc_slices(d);
-    tc::Params p{};
+    tcd::Params p{};
     p.mode = 0;
     p.dk = d;
     p.n_items = (int)(U * nvs);
@@ -1428,7 +1428,7 @@ static la_status tc_dense_pass(const void* q, const void* k, const void* v, void
     if (P > 1) {
         float* sums = reinterpret_cast<float*>(ws);
         float* starts = sums + (size_t)U * (P - 1) * d * d;
-        tc::Params p1 = p;
+        tcd::Params p1 = p;
         p1.n_seg = P - 1;
         p1.seg_base = reverse ? 1 : 0;  // the segments whose sums reach another segment's start
         p1.n_items = (int)(U * (P - 1) * nvs);

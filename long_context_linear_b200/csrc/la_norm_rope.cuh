@@ -23,6 +23,13 @@ la_status nrope_view(nrope::View* out, const la_view* v, const char* name, size_
     return LA_OK;
 }
 
+// An output whose entries share memory would be written by several blocks.
+la_status nrope_distinct(const nrope::View& v, const char* name, int B, int H, int N) {
+    if ((B > 1 && v.sb == 0) || (H > 1 && v.sh == 0) || (N > 1 && v.sn == 0))
+        return fail(LA_ERR_INVALID_ARG, "%s: stride 0 in a dimension of more than one entry", name);
+    return LA_OK;
+}
+
 // Checks shared by both directions; fills everything but the views.
 la_status nrope_common(nrope::Params* p, const void* q_weight, const void* k_weight, const float* inv_freq,
                        const void* positions, int pos64, int64_t pos_sb, int64_t pos_sn, int B, int N, int Hq, int Hk,
@@ -60,10 +67,11 @@ la_status nrope_common(nrope::Params* p, const void* q_weight, const void* k_wei
     return LA_OK;
 }
 
-// Rows per thread: 4, or 1 when that leaves SMs without a block, or when so
-// many rows would be so many tokens (few heads) that their angles do not fit
-// (norm + rotation of 64 tokens of 64 + 64 heads of 128: 5.1 us with 4, 3.9 with 1).
-constexpr int kNropeFewHeads = 4;
+// Rows per thread: 4 (backward 2), or 1 when that leaves SMs without a block
+// (norm + rotation of 64 tokens of 64 + 64 heads of 128: 5.1 us with 4, 3.9 with
+// 1), and forward for a side of one head, whose rows are as many tokens with
+// angles of their own (4 x 8192 tokens of 64 + 1 heads of 128: 270 us with 1, 281
+// with 4; 3 + 3 fp32 heads 56 and 48; backward 603 and 518 with 2).
 
 // Launches a direction; `most`: at most this many blocks (0: one per pass).
 // On the way it fixes the number of blocks of either side.
@@ -71,7 +79,7 @@ template <typename T, int D>
 void nrope_launch(nrope::Params& p, bool inter, bool backward, long most, int sms, cudaStream_t st) {
     const long rows = p.side[0].rows + p.side[1].rows;
     bool few = rows <= (long)sms * nrope::block_rows<T, D, 4>();
-    for (const nrope::Side& sd : p.side) few = few || (sd.rows && sd.H < kNropeFewHeads);
+    for (const nrope::Side& sd : p.side) few = few || (!backward && sd.rows && sd.H == 1);
     const int per = few ? nrope::block_rows<T, D, 1>() : nrope::block_rows<T, D, 4>() / (backward ? 2 : 1);
     size_t smem = 0;
     long n[2];
@@ -121,9 +129,11 @@ la_status la_qk_norm_rope(const la_view* q, const la_view* k, const la_view* q_o
     if (s != LA_OK) return s;
     if (p.side[0].rows + p.side[1].rows == 0) return LA_OK;
     const size_t esz = dt == LA_FP32 ? 4 : 2;
-    if (Hq && ((s = nrope_view(&p.side[0].x, q, "q", esz)) != LA_OK || (s = nrope_view(&p.side[0].y, q_out, "q_out", esz)) != LA_OK))
+    if (Hq && ((s = nrope_view(&p.side[0].x, q, "q", esz)) != LA_OK || (s = nrope_view(&p.side[0].y, q_out, "q_out", esz)) != LA_OK ||
+               (s = nrope_distinct(p.side[0].y, "q_out", B, Hq, N)) != LA_OK))
         return s;
-    if (Hk && ((s = nrope_view(&p.side[1].x, k, "k", esz)) != LA_OK || (s = nrope_view(&p.side[1].y, k_out, "k_out", esz)) != LA_OK))
+    if (Hk && ((s = nrope_view(&p.side[1].x, k, "k", esz)) != LA_OK || (s = nrope_view(&p.side[1].y, k_out, "k_out", esz)) != LA_OK ||
+               (s = nrope_distinct(p.side[1].y, "k_out", B, Hk, N)) != LA_OK))
         return s;
     DeviceInfo* di;
     if ((s = device_info(&di)) != LA_OK) return s;
@@ -155,11 +165,13 @@ la_status la_qk_norm_rope_backward(const la_view* dq_out, const la_view* dk_out,
     if (any) {
         if (Hq && ((s = nrope_view(&p.side[0].x, q, "q", esz)) != LA_OK ||
                    (s = nrope_view(&p.side[0].dy, dq_out, "dq_out", esz)) != LA_OK ||
-                   (s = nrope_view(&p.side[0].y, dq, "dq", esz)) != LA_OK))
+                   (s = nrope_view(&p.side[0].y, dq, "dq", esz)) != LA_OK ||
+                   (s = nrope_distinct(p.side[0].y, "dq", B, Hq, N)) != LA_OK))
             return s;
         if (Hk && ((s = nrope_view(&p.side[1].x, k, "k", esz)) != LA_OK ||
                    (s = nrope_view(&p.side[1].dy, dk_out, "dk_out", esz)) != LA_OK ||
-                   (s = nrope_view(&p.side[1].y, dk, "dk", esz)) != LA_OK))
+                   (s = nrope_view(&p.side[1].y, dk, "dk", esz)) != LA_OK ||
+                   (s = nrope_distinct(p.side[1].y, "dk", B, Hk, N)) != LA_OK))
             return s;
     }
     const size_t need = la_qk_norm_rope_backward_workspace_size(d);

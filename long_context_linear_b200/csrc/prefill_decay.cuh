@@ -49,6 +49,7 @@
 // stops the CTA cleanly.
 #pragma once
 #include "decay.cuh"
+#include "f32x2.cuh"
 #include "prefill_tc.cuh"
 
 namespace lcl {
@@ -57,6 +58,17 @@ namespace tcd {
 using tc::C;
 using tc::DVS;
 using tc::PANEL;
+
+struct Params : tc::Params {
+    const float* log_decay;  // [H] log of the decay per head, or null (prefill_tc.cuh's kernels); dense: head u % H
+    // dense whole sequences: chunks per CTA of the wrapped schedule (0: items in
+    // turn), the states handed on from CTA to CTA [grid][DK][DVS] and how many
+    // warps have written each (zero at launch)
+    int wrap;
+    float* wrap_state;
+    int* wrap_ready;
+};
+
 constexpr int SLOTS = 2;                    // Q, K, V ring depth
 constexpr int TERMS = 3;                    // bf16 terms of the weighted V
 constexpr int TILE = 2 * PANEL;             // Q, K: two 64-column panels
@@ -215,7 +227,7 @@ struct Piece : tc::Item {
     int from, to;       // CTA whose state is continued, own slot written for the next one (or -1)
 };
 template <int KD, bool kRev, bool kLean>
-__device__ __noinline__ Piece piece(const tc::Params& p, int r, int cta, int G) {
+__device__ __noinline__ Piece piece(const Params& p, int r, int cta, int G) {
     constexpr int NV = KD / DVS;
     constexpr long SLOT = (long)KD * DVS;
     Piece it;
@@ -272,7 +284,7 @@ __device__ __noinline__ bool wait_state(const int* ready) {
     return false;
 }
 // lam^n as two fp32 values, for the head of `it`
-__device__ __noinline__ float2 item_power(const tc::Params& p, int c1, int c2, int n) {
+__device__ __noinline__ float2 item_power(const Params& p, int c1, int c2, int n) {
     float2 f;
     decay::power2(p.log_decay[p.mode == 0 ? c2 % p.H : c1], n, f.x, f.y);
     return f;
@@ -285,7 +297,7 @@ template <int KD, bool kRev, bool kLean>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
-                     const __grid_constant__ tc::Params p) {
+                     const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);

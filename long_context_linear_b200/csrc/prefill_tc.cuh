@@ -127,13 +127,6 @@ struct Params {
     const int* seg_off_nl;
     const int* seg_len_dev;
     int n_seq;
-    const float* log_decay; // [H] log of the decay per head (prefill_decay.cuh), or null; dense: head u % H
-    // prefill_decay.cuh, dense whole sequences only: chunks per CTA of the
-    // wrapped schedule (0: items in turn), the states handed on from CTA to CTA
-    // [grid][DK][DVS] and how many warps have written each (zero at launch)
-    int wrap;
-    float* wrap_state;
-    int* wrap_ready;
 };
 
 struct Item {

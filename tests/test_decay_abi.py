@@ -98,6 +98,14 @@ def test_norm_rope_refuses(abi, kw, status, backward):
     assert abi.lib.la_last_error()
 
 
+@pytest.mark.parametrize("view", [dict(sb=0), dict(sh=0), dict(sn=0)])
+def test_norm_rope_refuses_outputs_that_share_memory(abi, view):
+    assert _norm_rope(abi, qo=view) == 1 and b"q_out" in abi.lib.la_last_error()
+    if "sh" not in view:  # (one key head: its stride says nothing)
+        assert _norm_rope(abi, ko=view) == 1 and b"k_out" in abi.lib.la_last_error()
+    assert _norm_rope(abi, True, q=view) == 1 and b"dq" in abi.lib.la_last_error()
+
+
 @pytest.mark.parametrize("kw", [dict(ws=None), dict(ws=FAKE + 8), dict(wsb=64), dict(gw=FAKE + 2)])
 def test_norm_rope_backward_refuses_its_own(abi, kw):
     assert _norm_rope(abi, True, **kw) == 1
