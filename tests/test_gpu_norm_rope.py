@@ -96,6 +96,13 @@ def test_sizes(la, B, N, Hq, Hk, dtype):
     check(la, *x, 128, np.arange(N), dtype, False)
 
 
+@pytest.mark.parametrize("dtype,Hq,Hk", [("bf16", 1, 2), ("bf16", 3, 1), ("fp32", 2, 1)])
+def test_many_tokens_of_few_heads(la, dtype, Hq, Hk):
+    # (enough rows for several of them per thread)
+    x = inputs(4, 5003, Hq, Hk, 64, dtype, seed=7)
+    check(la, *x, 32, np.arange(5003), dtype, False)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_far_positions_of_each_sequence(la, dtype):
     """Angles of 10^9 radians: the frequencies are fp32 values, their products with the position are exact in double."""
