@@ -49,7 +49,7 @@
 // stops the CTA cleanly.
 //
 // Bound by instruction fetch: the roles of all SMs run different code at once,
-// and the instruction cache that SMs share is 83 % busy at 37 % of the tensor
+// and the instruction cache that SMs share is 70 % busy at 42 % of the tensor
 // pipe.  Measured at B=1 H=64 N=16K, d = 128 (128 CTAs): 0.29 ms, 2.26 us per
 // chunk of 128 tokens (without a decay 1.64, the bytes at the copy rate 1.28);
 // B=4 H=32 N=8K: 0.29 ms = 3.7 TB/s, 0.56 of the copy rate.
