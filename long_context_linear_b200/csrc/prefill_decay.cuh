@@ -89,7 +89,13 @@ constexpr int OFF_S = OFF_VT + 2 * VT_BUF;
 constexpr int OFF_OST = OFF_S + PANEL;
 constexpr int OFF_BAR = OFF_OST + PANEL;
 static_assert(OFF_VT % 1024 == 0 && OFF_S % 1024 == 0 && VT_PANEL % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-// mbarriers (8 bytes each) at OFF_BAR, then the TMEM base
+// mbarriers (8 bytes each) at OFF_BAR, then the TMEM base.  A wait knows a phase
+// by its parity alone, so no barrier may complete a second phase while a warp has
+// yet to see the first: whoever waits on one also takes part in its next phase
+// (directly, or in a step that its arrivals wait for).  With [2] the next phase is
+// that of chunk g + 2; a single o_empty would break the rule, as thread A comes to
+// it only two chunks later and chunk g + 1 goes on without A once its Q K^T is
+// issued.  [4] are once per chunk each, like the single ones.
 constexpr int BAR_Q_FULL = 0;                      // [2] TMA -> A, C
 constexpr int BAR_Q_EMPTY = BAR_Q_FULL + SLOTS;    // [2] A (Q K^T) + C (Q S) -> TMA
 constexpr int BAR_K_FULL = BAR_Q_EMPTY + SLOTS;    // [2] TMA -> A, B, P warps (ragged tail)
@@ -101,8 +107,8 @@ constexpr int BAR_VT_EMPTY = BAR_VT_FULL + 4;      // [4] by quarter: B (its pro
 constexpr int BAR_P_FULL = BAR_VT_EMPTY + 4;       // [2] A (Q K^T) -> P warps
 constexpr int BAR_P_READY = BAR_P_FULL + 2;        // [2] P warps (bf16 P written, V landed) -> C
 constexpr int BAR_O_FULL = BAR_P_READY + 2;        // C (P V, Q S) -> output warps, state warps
-constexpr int BAR_O_EMPTY = BAR_O_FULL + 1;        // output warps (Opv, Oqs read) -> A, C
-constexpr int BAR_DS_FULL = BAR_O_EMPTY + 1;       // B -> state warps
+constexpr int BAR_O_EMPTY = BAR_O_FULL + 1;        // [2] output warps (Opv, Oqs read) -> A (two chunks later), C (the next)
+constexpr int BAR_DS_FULL = BAR_O_EMPTY + 2;       // B -> state warps
 constexpr int BAR_DS_EMPTY = BAR_DS_FULL + 1;      // state warps -> B
 constexpr int BAR_S_FULL = BAR_DS_EMPTY + 1;       // state warps (bf16(S) written) -> C
 constexpr int BAR_TAB = BAR_S_FULL + 1;            // P warps (decay table of an item written) -> P warps
@@ -354,9 +360,9 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             mbar_init(&v_empty[i], state_only ? 8 : 9);
             mbar_init(&p_full[i], 1);
             mbar_init(&p_ready[i], 4);
+            mbar_init(&o_empty[i], 4);
         }
         mbar_init(o_full, 1);
-        mbar_init(o_empty, 4);
         mbar_init(ds_full, 1);
         mbar_init(ds_empty, 4);
         mbar_init(s_full, 4);
@@ -439,7 +445,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 for (int g = 0; g < total; ++g) {
                     // once O of chunk g-2 has been read out of the buffer
                     const int s = g & 1;
-                    if (g > 1 && !wait(o_empty, g & 1)) break;
+                    if (g > 1 && !wait(&o_empty[s], ((g - 2) >> 1) & 1)) break;
                     if (!wait(&q_full[s], (g >> 1) & 1)) break;
                     if (!wait(&k_full[s], (g >> 1) & 1)) break;
                     tc_fence_after();
@@ -490,7 +496,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                         mma_ts(tp + TM_OPV, tp + kk * 8, dv + tc::mnmaj_step(kk), id_pv, kk > 0);
                     mma_commit(&v_empty[s]);
                     // (Q has landed: Q K^T has read it)
-                    if (g > 0 && !wait(o_empty, (g - 1) & 1)) break;
+                    if (g > 0 && !wait(&o_empty[s ^ 1], ((g - 1) >> 1) & 1)) break;
                     if (!wait(s_full, g & 1)) break;
                     tc_fence_after();
                     const uint64_t da = tc::kmaj_desc(sq + s * TILE, 0, PANEL);
@@ -768,7 +774,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     if (h == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(o_empty);
+                        if (lane == 0) mbar_arrive(&o_empty[s]);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
