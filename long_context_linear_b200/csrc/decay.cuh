@@ -27,9 +27,16 @@ __device__ __forceinline__ float power(double g, int n) { return n == 0 ? 1.f : 
 // lam^n as the sum of two fp32 values.  A state lives through thousands of
 // chunks: with slow decay one fp32 factor, 3e-8 off at worst, would repeat its
 // error as often (1024 chunks: 3e-5).
+//
+// Both values are positive (as long as lam^n is above 2^-126): hi is below lam^n,
+// never equal to it (1 is 1 - 2^-24 and 2^-24), so that an infinite state stays
+// infinite: x hi + x lo with a lo of zero would be infinity times zero, with a
+// negative one infinity minus infinity.  For a finite x the sum is as good: the
+// fused x hi + (x lo) is rounded once, and for lam^n = 1 it is x.
 __device__ __forceinline__ void power2(double g, int n, float& hi, float& lo) {
     const double f = n == 0 ? 1.0 : exp(g * n);
-    hi = static_cast<float>(f);
+    hi = __double2float_rz(f);
+    if (hi > 0.f && hi == f) hi = __uint_as_float(__float_as_uint(hi) - 1u);
     lo = static_cast<float>(f - hi);
 }
 

@@ -532,7 +532,8 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             // the item's table; the other one may still be read by a warp at the
             // item before, and nobody is two items behind (each waits here)
             float* tab = reinterpret_cast<float*>(sm + OFF_TAB) + (r & 1) * TAB + TAB_PAD;
-            tab[t + 1] = power(t + 1).x;
+            const float2 f1 = power(t + 1);
+            tab[t + 1] = f1.x + f1.y;
             if (t == 0) tab[0] = 1.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(tab_full);
