@@ -290,11 +290,19 @@ LA_API la_status la_prefill_backward_ex(const void* q, const void* k, const void
  *     S_t = exp(g_h) S_{t-1} + k_t (x) v_t,   o_t = q_t S_t
  *
  * with log_decay = g: fp32 device [H] (4-byte aligned), one value per head h,
- * g_h <= 0; g_h = 0 gives the calls without a decay, g_h = -infinity forgets
- * everything (S_t = k_t (x) v_t).  The values are a precondition; a positive or
- * NaN one is found only under LA_VALIDATE=1 (device-to-host copy and a stream
- * sync).  g is a constant of the layer: there is no gradient for it.  The
- * feature map is the identity.
+ * g_h <= 0; g_h = 0 gives what the calls without a decay give (of finite k and
+ * v), g_h = -infinity forgets everything (S_t = k_t (x) v_t).  The values are a
+ * precondition; a positive or NaN one is found only under LA_VALIDATE=1
+ * (device-to-host copy and a stream sync).  g is a constant of the layer: there
+ * is no gradient for it.  The feature map is the identity.
+ *
+ * Values that are not finite: an infinite state stays infinite for as long as
+ * exp(n g) is above 2^-126 over the n tokens of a chunk (128 on the tensor cores,
+ * at most 64 else), a segment or a step; below that it becomes NaN.  An infinite
+ * k or v makes the state entries that it reaches infinite on the FFMA path and
+ * infinite or NaN on the tensor cores, whose state update reads v in three parts.
+ * A v that is not finite also reaches its column of the outputs of earlier
+ * tokens of the same chunk, as in the calls without a decay.
  *
  * la_prefill_decay, la_prefill_varlen_decay and la_decode_step_decay are
  * la_prefill, la_prefill_varlen and la_decode_step_ex with that recurrence: the

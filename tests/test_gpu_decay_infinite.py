@@ -1,6 +1,7 @@
 """Infinite values in the decayed attention: a state that holds an infinity (an
 fp16 one overflows at 65504) keeps it, as the recurrence says and as the calls
-without a decay do."""
+without a decay do.  An infinite key or value makes the state entries that it
+reaches infinite, or NaN on the tensor cores, and nothing else."""
 import numpy as np
 import pytest
 import torch
@@ -95,3 +96,78 @@ def test_backward_keeps_infinite_state_gradients(la, dtype, d):
         ref = od.backward(q, k, v, do, G, None, ds)
     for a, b in zip(got, ref):
         same_kind(a.cpu(), b)
+
+
+def kind_by_path(got, ref, dtype):
+    """The recurrence's kind on the FFMA kernel; on the tensor cores NaN may stand for an infinity."""
+    if dtype == "fp32":
+        same_kind(got, ref)
+    else:
+        np.testing.assert_array_equal(np.isfinite(to64(got)), np.isfinite(to64(ref)))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 64)])
+@pytest.mark.parametrize("segments", ["1", "3"])
+@pytest.mark.parametrize("at", [150, 255, 390])
+def test_an_infinite_value(la, monkeypatch, dtype, d, segments, at):
+    """Only the value's column is touched, in the chunk of its token and later ones."""
+    monkeypatch.setenv("LA_PREFILL_SEGMENTS", segments)
+    q, k, v = synth.dense(1, 3, 400, d, dtype, seed=7)
+    v[:, :, at, 7] = INF
+    o, S = la.prefill(*cuda(q, k, v), log_decay=G.cuda())
+    with np.errstate(invalid="ignore"):
+        ro, rS = od.recurrent(q, k, v, G)
+    kind_by_path(S.cpu(), rS, dtype)
+    finite_close(S.cpu(), rS, 5e-6)
+    o, ro = to64(o.cpu()), to64(ro)
+    rest, first = np.arange(d) != 7, at // 128 * 128
+    for a, b in ((o[..., rest], ro[..., rest]), (o[:, :, :first], ro[:, :, :first])):
+        assert np.isfinite(a).all() and np.linalg.norm(a - b) <= 5e-3 * np.linalg.norm(b)
+    # from the token on the column is lost
+    assert not np.isfinite(o[:, :, at:, 7]).any()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 64)])
+@pytest.mark.parametrize("segments", ["1", "3"])
+@pytest.mark.parametrize("at", [150, 255, 390])
+def test_an_infinite_key(la, monkeypatch, dtype, d, segments, at):
+    """Every output from its token on is lost, those before it are right; of the state one row is lost."""
+    monkeypatch.setenv("LA_PREFILL_SEGMENTS", segments)
+    q, k, v = synth.dense(1, 3, 400, d, dtype, seed=8)
+    k[:, :, at, 7] = -INF
+    o, S = la.prefill(*cuda(q, k, v), log_decay=G.cuda())
+    with np.errstate(invalid="ignore"):
+        ro, rS = od.recurrent(q, k, v, G)
+    kind_by_path(S.cpu(), rS, dtype)
+    finite_close(S.cpu(), rS, 5e-6)
+    kind_by_path(o.cpu(), ro, dtype)
+    finite_close(o.cpu(), ro, 5e-3)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 64)])
+def test_an_infinite_output_gradient(la, dtype, d):
+    q, k, v = synth.dense(1, 3, 300, d, dtype, seed=9)
+    do = synth.dense(1, 3, 300, d, dtype, seed=10)[2]
+    do[:, :, 140, 7] = INF
+    _, dk, dv, ds0 = la.prefill_backward(*cuda(q, k, v, do), log_decay=G.cuda())
+    with np.errstate(invalid="ignore"):
+        _, rdk, rdv, rds0 = od.backward(q, k, v, do, G)
+    kind_by_path(ds0.cpu(), rds0, dtype)
+    kind_by_path(dk.cpu(), rdk, dtype)
+    kind_by_path(dv[:, :, :128].cpu(), rdv[:, :, :128], dtype)
+
+
+def test_an_infinite_value_in_a_packed_batch(la):
+    """Only the sequence that holds it is touched."""
+    d, lens = 128, [200, 70, 300]
+    cu = synth.cu_seqlens(lens)
+    q, k, v = synth.qkv((int(cu[-1]), 3, d), d, "bf16", seed=11)
+    v[250, :, 7] = INF
+    o, S = la.prefill_varlen(*cuda(q, k, v, cu), log_decay=G.cuda())
+    with np.errstate(invalid="ignore"):
+        ro, rS = od.varlen(q, k, v, cu, G)
+    kind_by_path(S.cpu(), rS, "bf16")
+    finite_close(S.cpu(), rS, 5e-6)
+    for part in (slice(0, 200), slice(270, None)):
+        finite_close(o[part].cpu(), ro[part], 5e-3)
+        assert torch.isfinite(o[part]).all()
