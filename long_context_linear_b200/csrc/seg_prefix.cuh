@@ -11,7 +11,8 @@
 //
 // kDecay: the sums carry their decay to the segment's end (in reverse order:
 // beyond its start), and the running state is multiplied by lam^len over each
-// segment it passes (decay.cuh): starts[p+1] = lam^len_p starts[p] + sum_p.
+// segment it passes (decay.cuh): starts[p+1] = lam^len_p starts[p] + sum_p.  The
+// factor is two fp32 values: one is up to 5e-8 off, as often as there are segments.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -21,6 +22,15 @@ namespace lcl {
 namespace segp {
 
 constexpr int NUM_THREADS = 256;
+
+// lam^len * acc + x
+struct Factor {
+    float hi, lo;
+    __device__ __forceinline__ float at(float acc, float x) const { return fmaf(acc, hi, fmaf(acc, lo, x)); }
+    __device__ __forceinline__ void pass(float4& acc, const float4& x) const {
+        acc.x = at(acc.x, x.x); acc.y = at(acc.y, x.y); acc.z = at(acc.z, x.z); acc.w = at(acc.w, x.w);
+    }
+};
 
 // seg_sums: [U][n_seg-1][elems]; s0: [U][elems] or null; starts: [U][n_seg][elems].
 // Forward: seg_sums[p] is the sum of segment p, starts[p] = s0 + sum_{p' < p}.
@@ -48,29 +58,26 @@ __device__ __forceinline__ void seg_prefix_body(const float* __restrict__ seg_su
         }
         float* dst = starts + (u * n_seg) * (long)elems + e;
         const float* src = seg_sums + (u * (n_seg - 1)) * (long)elems + e;
-        float f = 1.f, f_tail = 1.f;
+        Factor f{1.f, 0.f}, f_tail{1.f, 0.f};
         if constexpr (kDecay) {
             const double g = log_decay[u % H];
-            f = decay::power(g, seg_len);
-            f_tail = decay::power(g, tail_len);
+            decay::power2(g, seg_len, f.hi, f.lo);
+            decay::power2(g, tail_len, f_tail.hi, f_tail.lo);
         }
         if (!reverse) {
             *reinterpret_cast<float4*>(dst) = acc;
             for (int p = 1; p < n_seg; ++p) {
                 const float4 x = *reinterpret_cast<const float4*>(src + (long)(p - 1) * elems);
-                if constexpr (kDecay) { acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f; }
-                acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+                if constexpr (kDecay) f.pass(acc, x);
+                else { acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w; }
                 *reinterpret_cast<float4*>(dst + (long)p * elems) = acc;
             }
         } else {
             *reinterpret_cast<float4*>(dst + (long)(n_seg - 1) * elems) = acc;
             for (int p = n_seg - 2; p >= 0; --p) {
                 const float4 x = *reinterpret_cast<const float4*>(src + (long)p * elems);
-                if constexpr (kDecay) {
-                    const float fp = p == n_seg - 2 ? f_tail : f;
-                    acc.x *= fp; acc.y *= fp; acc.z *= fp; acc.w *= fp;
-                }
-                acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+                if constexpr (kDecay) (p == n_seg - 2 ? f_tail : f).pass(acc, x);
+                else { acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w; }
                 *reinterpret_cast<float4*>(dst + (long)p * elems) = acc;
             }
         }
@@ -124,12 +131,12 @@ seg_prefix_varlen_kernel(const float* __restrict__ seg_sums, const float* __rest
         if (pool && ii >= 0) acc = *reinterpret_cast<const float4*>(pool + ((long)ii * H + h) * elems + e);
         const int s0 = seg_off[r], cnt = seg_off[r + 1] - s0, nl0 = seg_off_nl[r];
         *reinterpret_cast<float4*>(starts + ((long)s0 * H + h) * elems + e) = acc;
-        float f = 1.f;  // every segment that another one follows has *seg_len tokens
-        if constexpr (kDecay) f = decay::power(log_decay[h], *seg_len);
+        Factor f{1.f, 0.f};  // every segment that another one follows has *seg_len tokens
+        if constexpr (kDecay) decay::power2(log_decay[h], *seg_len, f.hi, f.lo);
         for (int g = 1; g < cnt; ++g) {
             const float4 x = *reinterpret_cast<const float4*>(seg_sums + ((long)(nl0 + g - 1) * H + h) * elems + e);
-            if constexpr (kDecay) { acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f; }
-            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+            if constexpr (kDecay) f.pass(acc, x);
+            else { acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w; }
             *reinterpret_cast<float4*>(starts + ((long)(s0 + g) * H + h) * elems + e) = acc;
         }
     }
