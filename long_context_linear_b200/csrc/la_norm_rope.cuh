@@ -43,7 +43,9 @@ la_status nrope_common(nrope::Params* p, const void* q_weight, const void* k_wei
     if (rot < 0 || rot > d || rot % 16)
         return fail(LA_ERR_UNSUPPORTED, "rot = %d must be a multiple of 16 in [0, %d]", rot, d);
     if (!(eps >= 0.f) || eps > 1e30f) return fail(LA_ERR_INVALID_ARG, "eps must be finite and >= 0");
-    if (Hq > (1 << 20) || Hk > (1 << 20) || N > (1 << 30) || (long)B * N * ((long)Hq + Hk) > (1L << 34))
+    // (B * N * heads itself may pass 64 bits)
+    const long heads = (long)Hq + Hk;
+    if (Hq > (1 << 20) || Hk > (1 << 20) || N > (1 << 30) || (heads && (long)B * N > (1L << 34) / heads))
         return fail(LA_ERR_INVALID_ARG, "problem too large");
     if ((Hq && !q_weight) || (Hk && !k_weight)) return fail(LA_ERR_INVALID_ARG, "the weights must be non-null");
     if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(LA_ERR_INVALID_ARG, "the weights must be 16-byte aligned");
