@@ -80,6 +80,22 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _workspace(workspace: Optional[torch.Tensor], need: int, device: torch.device):
+    """A call's workspace and its bytes: the given one if it has `need` bytes, else a new one (None if need is 0).
+    The kernels write to a given one, so it has to be memory of the tensors' device."""
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError(f"workspace must be a tensor, got {type(workspace).__name__}")
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        size = workspace.numel() * workspace.element_size()
+        if size >= need:
+            return workspace, size
+    return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+
+
 def _check_decay(log_decay: torch.Tensor, H: int, device, phi: str = "identity"):
     """log_decay: fp32 [H] on the tensors' device, without a feature map."""
     _need(log_decay, "log_decay", torch.float32, device)
@@ -142,9 +158,7 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional[torc
             raise ValueError("out must be [B, H, N, dv] and s_out [B, H, dk, dv]")
     need = int(lib.la_prefill_workspace_size_ex(B, H, N, dk, dv, dt, _phi_code(phi)) if log_decay is None
                else lib.la_prefill_decay_workspace_size(B, H, N, dk, dv, dt))
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, need, q.device)
     with _on(q.device):
         if log_decay is not None:
             _abi.check(lib.la_prefill_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(s0), _ptr(s_out),
@@ -170,7 +184,9 @@ def prefill_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional
     device).  Asynchronous: synchronise that device's current stream before
     reading the results.
     """
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    dev = torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need_host(t, n, q.dtype)
     if q.dim() != 4 or k.shape != q.shape or v.shape[:3] != q.shape[:3]:
@@ -191,9 +207,7 @@ def prefill_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s0: Optional
     if s_out is not None:
         _need_host(s_out, "s_out", torch.float32)
     need = int(lib.la_prefill_host_workspace_size(B, H, N, dk, dv, dt, group))
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, max(need, 1), dev)
     with torch.cuda.device(dev):
         _abi.check(lib.la_prefill_host(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(s0), _ptr(s_out), B, H, N, dk, dv,
                                        dt, group, _ptr(workspace), ws_bytes, _stream(dev)), "la_prefill_host")
@@ -227,9 +241,7 @@ def prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dout: to
     ds0 = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if need_ds0 else None
     need = int((lib.la_prefill_backward_workspace_size if log_decay is None
                 else lib.la_prefill_decay_backward_workspace_size)(B, H, N, d, d, _dtype_code(q)))
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, need, q.device)
     with _on(q.device):
         if log_decay is not None:
             _abi.check(lib.la_prefill_decay_backward(
@@ -299,9 +311,7 @@ def prefill_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     if s_out is None and return_state:
         s_out = torch.empty((max(n_seq, 0), H, dk, dv), dtype=torch.float32, device=q.device)
     need = int(lib.la_prefill_varlen_workspace_size_ex(n_seq, T, H, dk, dv, dt, _phi_code(phi)))
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, need, q.device)
     with _on(q.device):
         if log_decay is not None:
             _abi.check(lib.la_prefill_varlen_decay(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(cu_seqlens), n_seq, T,
@@ -545,9 +555,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in range(2))
     with _on(q.device):
         need = int(lib.la_qk_norm_rope_backward_workspace_size(d))
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_bytes = workspace.numel() * workspace.element_size()
+        workspace, ws_bytes = _workspace(workspace, need, q.device)
         _abi.check(lib.la_qk_norm_rope_backward(*views[:4], _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
                                                 _ptr(positions), pos64, psb, psn, *views[4:], _ptr(dqw), _ptr(dkw), B,
                                                 N, Hq, Hk, d, rot, eps, int(interleaved), dt, wdt, _ptr(workspace),
