@@ -26,7 +26,7 @@ __all__ = ["prefill", "prefill_host", "prefill_varlen", "prefill_varlen_noalloc"
            "decode_verify",
            "decode_commit", "qk_norm_rope", "qk_norm_rope_backward",
            "device_status", "LAError",
-           "lib", "prefill_workspace_size", "prefill_varlen_workspace_size"]
+           "lib", "prefill_workspace_size", "prefill_varlen_workspace_size", "prefill_backward_workspace_size"]
 
 _DT = {torch.bfloat16: _abi.LA_BF16, torch.float32: _abi.LA_FP32}
 PHI = {"identity": _abi.LA_PHI_IDENTITY, "elu1": _abi.LA_PHI_ELU1, "relu": _abi.LA_PHI_RELU}
@@ -114,12 +114,25 @@ def _need_host(t: torch.Tensor, name: str, dtype=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def prefill_workspace_size(B: int, H: int, N: int, d: int, dtype: torch.dtype, phi: str = "identity") -> int:
+def prefill_workspace_size(B: int, H: int, N: int, d: int, dtype: torch.dtype, phi: str = "identity", *,
+                           decay: bool = False) -> int:
+    """Bytes of workspace that ``prefill`` asks for (decay: with log_decay)."""
+    if decay:
+        if phi != "identity":
+            raise ValueError("a decay needs phi='identity'")
+        return int(lib.la_prefill_decay_workspace_size(B, H, N, d, d, _DT[dtype]))
     return int(lib.la_prefill_workspace_size_ex(B, H, N, d, d, _DT[dtype], _phi_code(phi)))
+
+
+def prefill_backward_workspace_size(B: int, H: int, N: int, d: int, dtype: torch.dtype, *, decay: bool = False) -> int:
+    """Bytes of workspace that ``prefill_backward`` asks for (decay: with log_decay)."""
+    return int((lib.la_prefill_decay_backward_workspace_size if decay else lib.la_prefill_backward_workspace_size)(
+        B, H, N, d, d, _DT[dtype]))
 
 
 def prefill_varlen_workspace_size(n_seq: int, T: int, H: int, d: int, dtype: torch.dtype,
                                   phi: str = "identity") -> int:
+    """Bytes of workspace that ``prefill_varlen`` asks for, with or without log_decay."""
     return int(lib.la_prefill_varlen_workspace_size_ex(n_seq, T, H, d, d, _DT[dtype], _phi_code(phi)))
 
 
