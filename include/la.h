@@ -318,7 +318,8 @@ LA_API la_status la_prefill_backward_ex(const void* q, const void* k, const void
  * The workspaces are optional, as there, and their sizes are these calls' own:
  * with them, bf16 batches of more (head, 64 value columns) items than SMs are
  * shared out by chunks of 128 tokens instead of whole sequences (the same bits,
- * in less time).  One workspace serves one call at a time.
+ * in less time; a cooperative launch, for which whole sequences stand in where the
+ * context has fewer SMs than the device).  One workspace serves one call at a time.
  */
 LA_API size_t la_prefill_decay_workspace_size(int B, int H, int N, int dk, int dv, la_dtype dt);
 LA_API la_status la_prefill_decay(const void* q, const void* k, const void* v, void* o, const float* s0, float* s_out,

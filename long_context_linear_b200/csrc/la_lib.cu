@@ -315,7 +315,13 @@ la_status launch_tc(int grid, const CUtensorMap& mq, const CUtensorMap& mk, cons
             cfg.stream = st;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
-            (void)cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p);  // (an error is after_launch's)
+            if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p) != cudaErrorCooperativeLaunchTooLarge) return;
+            // (a context of fewer SMs than the device has: whole items in turn,
+            // whose CTAs wait for nothing; any other error is after_launch's)
+            (void)cudaGetLastError();
+            tcd::Params whole = p;
+            whole.wrap = 0;
+            kern<<<grid, tcd::NUM_THREADS, tcd::SMEM_BYTES, st>>>(mq, mk, mv, mo, whole);
         };
         const bool lean = p.mode == 0 && !p.state_only;
         if (p.dk == 64) {
