@@ -608,12 +608,16 @@ la_status check_log_decay(const float* log_decay, int H, cudaStream_t st) {
     if (!log_decay) return fail(LA_ERR_INVALID_ARG, "log_decay must be non-null");
     if (reinterpret_cast<uintptr_t>(log_decay) & 3u) return fail(LA_ERR_INVALID_ARG, "log_decay must be 4-byte aligned");
     if (!env_validate() || H <= 0) return LA_OK;
-    std::vector<float> g(H);
-    cudaError_t e = cudaMemcpyAsync(g.data(), log_decay, sizeof(float) * H, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return cuda_fail(e, "LA_VALIDATE copy of log_decay");
-    for (int h = 0; h < H; ++h)
-        if (!(g[h] <= 0.f)) return fail(LA_ERR_INVALID_ARG, "log_decay[%d] = %g is not <= 0", h, (double)g[h]);
+    // (in pieces: no allocation, which may throw through the C entry)
+    float g[256];
+    for (int h0 = 0; h0 < H; h0 += 256) {
+        const int n = std::min(256, H - h0);
+        cudaError_t e = cudaMemcpyAsync(g, log_decay + h0, sizeof(float) * n, cudaMemcpyDeviceToHost, st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+        if (e != cudaSuccess) return cuda_fail(e, "LA_VALIDATE copy of log_decay");
+        for (int i = 0; i < n; ++i)
+            if (!(g[i] <= 0.f)) return fail(LA_ERR_INVALID_ARG, "log_decay[%d] = %g is not <= 0", h0 + i, (double)g[i]);
+    }
     return LA_OK;
 }
 
