@@ -358,7 +358,8 @@ typedef struct {
  * (a cos - b sin, b cos + a sin), i < rot / 2; pairs are dims (i, i + rot/2), or
  * (2i, 2i + 1) with interleaved != 0; dims from rot on are only normed.  The
  * angle is formed in double (positions of millions keep theirs), everything
- * else in fp32 with one rounding to `dt`.
+ * else in fp32 with one rounding to `dt` (the sum of squares too: it overflows,
+ * and the row becomes zero, from values of 10^18 on).
  *   q, q_out: Hq heads;  k, k_out: Hk heads (either may be 0)   dtype `dt`,
  *          d in {64, 128}, any strides that keep rows 16-byte aligned: q and k
  *          may be slices of one projection's output, q_out and k_out the
@@ -382,8 +383,9 @@ LA_API la_status la_qk_norm_rope(const la_view* q, const la_view* k, const la_vi
  * Its gradients: given dq_out and dk_out (same shapes as q and k, any such
  * strides) it forms the norms again from q and k and writes dq, dk (dtype `dt`,
  * any such strides) and dq_weight, dk_weight (fp32 [d], or NULL: not wanted).
- * The weight gradients are summed in a fixed order.  workspace: at least
- * la_qk_norm_rope_backward_workspace_size(d) bytes (device, 16-byte aligned).
+ * The weight gradients are summed in fp32 in a fixed order.  workspace: at least
+ * la_qk_norm_rope_backward_workspace_size(d) bytes (device, 16-byte aligned); one
+ * workspace serves one call at a time.
  */
 LA_API size_t la_qk_norm_rope_backward_workspace_size(int d);
 LA_API la_status la_qk_norm_rope_backward(const la_view* dq_out, const la_view* dk_out, const la_view* q,

@@ -239,8 +239,9 @@ __device__ __forceinline__ void load_weight(const Params& p, const void* weight,
 
 // U rows per thread: 4 for many rows (bytes in flight), 1 for few.  4 x 8192
 // tokens of 32 + 32 bf16 heads of 128, from the projection's layout to the
-// attention's, all dims turned: 0.199 ms, 5.4 TB/s = 0.83 of a copy (norm alone
-// 0.188); 2 rows per thread 0.208.
+// attention's, all dims turned: 0.199 ms, 5.4 TB/s = 0.83 of a copy, for calls in
+// a row (norm alone 0.188; 2 rows per thread 0.208); 0.213 to 0.219 ms between
+// other work.
 template <typename T, int D, bool kInter, int U>
 __global__ void __launch_bounds__(NUM_THREADS, 6)
 norm_rope_kernel(const __grid_constant__ Params p) {
@@ -299,8 +300,9 @@ norm_rope_kernel(const __grid_constant__ Params p) {
 }
 
 // Gradients of q or k, and per block the sums of g xh over its rows (fixed
-// order: a block's rows depend on the grid alone).  The same size: 0.349 ms,
-// 4.6 TB/s = 0.70 of a copy: 32 accumulators and weights leave 128 registers and
+// order: a block's rows depend on the grid alone).  The same size, with the join
+// of the sums below: 0.349 ms in a row, 4.6 TB/s = 0.70 of a copy (2 x 4096 tokens,
+// half turned: 0.105 ms, 0.58): 32 accumulators and weights leave 128 registers and
 // 16 warps per SM, whose loads and arithmetic overlap across blocks only
 // (1 row per thread 0.44, fewer blocks per SM 0.39).
 template <typename T, int D, bool kInter, int U>
@@ -401,7 +403,10 @@ norm_rope_backward_kernel(const __grid_constant__ Params p) {
 }
 
 // dw = sum of the blocks' partial sums [blocks_q + blocks_k][d]: block (x, side)
-// takes 32 columns, 4 warps over the partial rows, joined in a fixed order.
+// takes 32 columns, 4 warps over the partial rows, joined in a fixed order.  With
+// the full grid of partial rows (1184) 29 us of a profiled (cold) call of 2 x 4096
+// tokens, beside 84 of the first kernel: d / 32 x 2 blocks on an empty GPU, each
+// warp's 148 loads one after another.
 __global__ void __launch_bounds__(NUM_THREADS)
 weight_grad_kernel(const float* __restrict__ partial, int blocks_q, int blocks_k, int d, float* __restrict__ dwq,
                    float* __restrict__ dwk) {

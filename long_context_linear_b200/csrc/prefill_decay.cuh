@@ -52,11 +52,17 @@
 // is terms -> dS -> S -> Q S.  Every wait is bounded (wait_bounded); a timeout
 // stops the CTA cleanly.
 //
-// Bound by instruction fetch: the roles of all SMs run different code at once,
-// and the instruction cache that SMs share is 70 % busy at 42 % of the tensor
-// pipe.  Measured at B=1 H=64 N=16K, d = 128 (128 CTAs): 0.29 ms, 2.26 us per
-// chunk of 128 tokens (without a decay 1.64, the bytes at the copy rate 1.28);
-// B=4 H=32 N=8K: 0.29 ms = 3.7 TB/s, 0.56 of the copy rate.
+// Measured at B=1 H=64 N=16K, d = 128 (128 CTAs): 0.29 ms, 2.26 us per chunk of
+// 128 tokens (without a decay 1.64, the bytes at the copy rate 1.28); B=4 H=32
+// N=8K: 0.28 to 0.29 ms = 3.7 TB/s, 0.56 of the copy rate, for some tens of calls
+// in a row, 0.34 to 0.35 ms between other work (cold L2, lower clock).
+// What bounds it: neither the bytes (38 % of DRAM's rate) nor the tensor pipe
+// (42 % busy).  Its code size matters: with everything unrolled a chunk took 5.4
+// us, the cache of instructions that SMs share is still 70 % busy, and 64 more
+// instructions in the state warps cost 7 to 25 %.  But few stalls are for a
+// missing instruction (0.5 per issue, against 3.1 for long scoreboards): how
+// much of a chunk is the chain of its steps is not measured.  128 registers a
+// thread spill 100 to 180 bytes.
 #pragma once
 #include "decay.cuh"
 #include "f32x2.cuh"
@@ -222,7 +228,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
 }
 
 // Out of line, one copy for all roles: they run once per item, and the
-// kernel's instruction footprint is what its loops wait for (all roles of all
+// kernel's instruction footprint counts (all roles of all
 // SMs run at once; with these inlined and everything unrolled it was 112 KB and
 // took 10,000 cycles per chunk).
 //
@@ -625,7 +631,7 @@ prefill_decay_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // ------------------------------------------------------ state warps
         const int q4 = warp & 3;
         const int i = q4 * 32 + lane;  // key-dim row of S owned by this thread
-        const bool own = KD == 128 || q4 < KD / 32;  // warp-uniform; at d = 64 warps 8, 9 only follow along
+        const bool own = KD == 128 || q4 < KD / 32;  // warp-uniform; at d = 64 warps 6, 7 (q4 = 2, 3) only follow along
         const uint32_t tds = tbase + (static_cast<uint32_t>(q4 * 32) << 16) + TM_DS;
         const uint32_t srow = smem_u32(sm + OFF_S) + static_cast<uint32_t>(i) * 128u;
         const int t = (warp - 6) * 32 + lane;
